@@ -1,6 +1,7 @@
 /*
  * pi.h -- C ABI of the predictor-gated, neuron-aware sparse FFN for AMD
- * Instinct MI355X (gfx950).
+ * Instinct MI355X (gfx950), and of the paged key/value cache and the attention
+ * over it, the other half of a decoder layer (second part of this file).
  *
  * The method (PowerInfer pages):
  *  - chatpaper.ai abstract; CSDN article, section on sparse activation: a
@@ -451,6 +452,211 @@ pi_status pi_copy(const void* src, void* dst, int64_t bytes, void* stream);
 #define PI_STREAM_SINK_WORDS 2048
 pi_status pi_stream_read(const void* src, int64_t bytes, uint32_t* sink, void* stream);
 
+/* ---- paged key/value cache and the attention over it -------------------------
+ *
+ * The other half of a decoder layer, for prompts in chunks and for single
+ * tokens.  A cache holds the keys and values of all layers in pages of
+ * page_size tokens; a sequence names its pages in a table, in order, so key j
+ * of a sequence lies in page table[j / page_size] at place j % page_size.
+ * Element types are PI_F32 and PI_F16 (q, k, v and the output have the cache's
+ * type).  The conventions at the head of this file hold; besides them:
+ *  - A table entry outside 0..pages-1 (e.g. -1) names no page: its keys are
+ *    seen by no row, and nothing is written to them.
+ *  - Device counts (lengths, first rows, page ids, lists) are never trusted
+ *    with an address: values out of range are clamped or ignored.
+ */
+enum { PI_MAX_HEAD_DIM = 256, PI_MAX_PAGE_SIZE = 1024 };
+
+/* k and v: [layers][pages][kv_heads][page_size][head_dim], 16-byte aligned: the
+ * keys of one head in one page are one contiguous block. */
+typedef struct pi_kv_cache {
+    int32_t dtype;        /* PI_F32 or PI_F16 */
+    int32_t layers;       /* >= 1 */
+    int32_t pages;        /* 1..2^24, per layer */
+    int32_t kv_heads;     /* 1..65535 */
+    int32_t page_size;    /* tokens per page: a power of two, 8..PI_MAX_PAGE_SIZE */
+    int32_t head_dim;     /* a multiple of 8, 8..PI_MAX_HEAD_DIM */
+    void* k;
+    void* v;
+} pi_kv_cache;
+
+/* A batch of sequences, each with some new tokens (its last ones).  Row t of
+ * q, k, v and the output belongs to sequence s with q_start[s] <= t <
+ * q_start[s+1] and is its token at position kv_len[s] - (q_start[s+1] - t).
+ * Rows that belong to no sequence are left as they are. */
+typedef struct pi_seq_batch {
+    int32_t n_seqs;         /* 0..2^20 */
+    int32_t n_tokens;       /* rows of q, 0..2^23 */
+    int32_t max_new;        /* most new tokens of one sequence; rows beyond it are not computed */
+    int32_t max_len;        /* most tokens of one sequence (a hint for the split of the work) */
+    const int32_t* q_start; /* [n_seqs + 1] device, ascending */
+    const int32_t* kv_len;  /* [n_seqs] device: tokens in the cache, the new ones included */
+    const int32_t* table;   /* [n_seqs][table_stride] device: page ids */
+    int32_t table_stride;   /* >= 1; a sequence is at most table_stride * page_size tokens long */
+} pi_seq_batch;
+
+/* One [n_tokens][heads][head_dim] tensor with strides in elements; the
+ * elements of a head are contiguous.  Base and strides 16-byte aligned. */
+typedef struct pi_rows {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} pi_rows;
+
+/* Rotary positions.  Pair i < rotary_dim / 2 of a head turns by turns[i] *
+ * position full turns: with a = 2 pi turns[i] position and m = magnitude
+ *   x0' = m (x0 cos a - x1 sin a),  x1' = m (x1 cos a + x0 sin a).
+ * Elements from rotary_dim on pass unchanged.  The product turns[i] * position
+ * is formed and reduced to a fraction of a turn in 64 bits (in 32 bits position
+ * 100000 is off by a hundredth of a radian), sin and cos in 32. */
+enum { PI_ROPE_HALVES = 0, PI_ROPE_PAIRS = 1 };  /* pairs (i, i + rotary_dim/2) or (2i, 2i + 1) */
+typedef struct pi_rope {
+    int32_t rotary_dim;   /* even, 0..head_dim */
+    int32_t layout;       /* PI_ROPE_HALVES or PI_ROPE_PAIRS */
+    const double* turns;  /* [rotary_dim / 2] device (pi_rope_turns); may be NULL iff rotary_dim == 0 */
+    float magnitude;
+} pi_rope;
+
+/* How pi_rope_turns stretches positions for contexts longer than the trained
+ * ones.  With f_i = base^(-2i / rotary_dim) (radians per position):
+ *   PI_SCALE_NONE      f_i
+ *   PI_SCALE_LINEAR    f_i / factor (positions interpolated)
+ *   PI_SCALE_BASE      base grown by factor^(rotary_dim / (rotary_dim - 2)): the fastest
+ *                      pair keeps its rate, the slowest is slowed by factor
+ *   PI_SCALE_BANDS     with r_i = context * f_i / 2 pi, the turns of pair i over the
+ *                      trained context: pairs with r_i >= high keep f_i, pairs with
+ *                      r_i <= low get f_i / factor, between them the weight of f_i is
+ *                      (r_i - low) / (high - low) */
+enum { PI_SCALE_NONE = 0, PI_SCALE_LINEAR = 1, PI_SCALE_BASE = 2, PI_SCALE_BANDS = 3 };
+
+/* turns [host, out] [rotary_dim / 2]: turns per position of each pair, f_i / 2 pi.
+ * Host arithmetic; nothing is enqueued.  PI_ERR_SHAPE: rotary_dim odd or outside
+ * 0..PI_MAX_HEAD_DIM; PI_ERR_ARG: base <= 1, factor < 1, not low < high, context
+ * <= 0 (the last two for PI_SCALE_BANDS only), an unknown scaling, NULL turns. */
+pi_status pi_rope_turns(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                        double low, double high, double context, double* turns);
+
+/*
+ * The new tokens' queries turned into q_out (may be q itself), their keys
+ * turned and written with their values into the pages of `layer`.  k and v
+ * have kv_heads heads, q and q_out q_heads (a multiple of kv_heads is not
+ * needed here; q->data and q_out->data may both be NULL: keys and values
+ * only).  positions [n_tokens] device int32, or NULL: the positions that turn
+ * q and k, where they are not the places in the cache (a negative position
+ * turns back).  k and v may not overlap the cache.  One kernel, no workspace.
+ */
+pi_status pi_rope_append(const pi_kv_cache* cache, int32_t layer, const pi_seq_batch* batch,
+                         const pi_rope* rope, const int32_t* positions, int32_t q_heads,
+                         const pi_rows* q, const pi_rows* q_out, const pi_rows* k,
+                         const pi_rows* v, void* stream);
+
+/* Which keys a row sees, and how a score is formed.  Row t at position pos of
+ * sequence s sees the keys lo <= j < hi:
+ *   lo = max(0, first[t] if first, pos - window + 1 if window > 0)
+ *   hi = min(kv_len[s], max(pos + 1, prefix[s] if prefix))
+ *   score = scale * q.k;  cap * tanh(score / cap) if cap > 0;
+ *           minus slopes[h] * |pos - j| if slopes */
+typedef struct pi_score_rule {
+    float scale;            /* finite */
+    float cap;              /* >= 0; 0: no cap */
+    int32_t window;         /* >= 0; 0: no window */
+    const float* slopes;    /* [q_heads] device or NULL */
+    const int32_t* prefix;  /* [n_seqs] device or NULL: tokens that all rows of a sequence see */
+    const int32_t* first;   /* [n_tokens] device or NULL: first key a row sees (documents packed
+                               into one sequence, padding at its head) */
+} pi_score_rule;
+
+/*
+ * Attention of the new tokens over the cache, their own keys included (write
+ * them first: pi_rope_append).  q_heads is a multiple of kv_heads; query head
+ * h reads key head h / (q_heads / kv_heads).
+ *   out[t][h] = sum_j w_j V[j] / sum_j w_j,  w_j = exp(score_j - max)
+ *   lse[t][h] (float32 [n_tokens][q_heads], or NULL) = max + ln sum_j w_j
+ * A row that sees no key gets zeros and lse = -inf.  Keys that a row does not
+ * see have no influence on it, whatever they hold (infinities and NaN
+ * included).  Scores, weights, sums and outputs are float32 until the output is
+ * rounded once; with PI_F16 the weights are rounded to f16 for the product with
+ * V (relative error 2^-12 each), their sum is not.  out may be q.
+ * Needs a workspace of pi_attention_workspace_bytes (256-byte aligned).
+ */
+size_t pi_attention_workspace_bytes(const pi_kv_cache* cache, const pi_seq_batch* batch,
+                                    int32_t q_heads);
+pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_seq_batch* batch,
+                             const pi_score_rule* rule, int32_t q_heads, const pi_rows* q,
+                             const pi_rows* out, float* lse, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * The pages' bookkeeping, all of it in device memory, so that beams can fork
+ * and sequences grow between two steps without the host waiting.
+ * refs[p] is the number of table entries that name page p; 0 = free.  Entries
+ * of a table row past its sequence's pages are -1.  A sequence of len tokens
+ * has ceil(len / page_size) pages.  (All -1, lens and refs 0 is an empty cache.)
+ */
+typedef struct pi_page_state {
+    int32_t pages;          /* 1..2^24 */
+    int32_t max_seqs;       /* rows of the table, 1..2^20 */
+    int32_t table_stride;   /* 1..2^24 */
+    int32_t page_size;      /* a power of two, 8..PI_MAX_PAGE_SIZE */
+    int32_t* refs;          /* [pages] */
+    int32_t* table;         /* [max_seqs][table_stride] */
+    int32_t* lens;          /* [max_seqs] */
+} pi_page_state;
+
+/* Workspace for the calls below with lists of up to n sequences (256-byte
+ * aligned); 0 if out of range (n in 0..max_seqs). */
+size_t pi_pages_workspace_bytes(const pi_page_state* state, int32_t n);
+
+/*
+ * Room for add[i] more tokens in sequence seqs[i], i < n (device int32 lists;
+ * each sequence at most once).  A sequence needs the pages its new length adds,
+ * and one more if its last page is partly filled and shared (refs > 1 when the
+ * call begins): that page is copied before it is written to, and the sequence
+ * gets the copy.  In list order, a sequence is granted its pages as long as
+ * the sum of the needs up to and including it is at most the number of free
+ * pages, and it takes the lowest free ones, first the copy, then the new
+ * ones; its length grows by add[i].  One that would pass table_stride pages
+ * needs nothing and is not granted, like one with add[i] < 0 or an id outside
+ * the table.
+ *   granted [n] int32, out: 1 or 0.
+ *   copies [2][n] int32, out: the copied page and its copy, or -1, -1.
+ *   cache: its pages are copied in every layer (cache->pages == state->pages,
+ *          same page_size); NULL: the caller copies (pi_pages_copy).
+ */
+pi_status pi_pages_extend(const pi_page_state* state, const pi_kv_cache* cache,
+                          const int32_t* seqs, const int32_t* add, int32_t n, int32_t* granted,
+                          int32_t* copies, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Sequence dst[i] becomes what src[i] was when the call began, i < n, all at
+ * once (beams that change parents: dst = 0..n-1, src = the parents; a new
+ * fork: dst = a row with no pages).  Pages are shared, not copied: the counts
+ * of src's pages grow, those of dst's old ones shrink.  dst without
+ * repetitions; pairs with an id outside the table are ignored.
+ */
+pi_status pi_pages_fork(const pi_page_state* state, const int32_t* src, const int32_t* dst,
+                        int32_t n, void* ws, size_t ws_bytes, void* stream);
+
+/* Sequences seqs[i], i < n (without repetitions), give up their pages: counts
+ * shrink, their rows become -1, their lengths 0. */
+pi_status pi_pages_free(const pi_page_state* state, const int32_t* seqs, int32_t n, void* stream);
+
+/*
+ * The pages in use become 0..live-1: of the pages in use with ids >= live, in
+ * ascending order, the i-th moves to the i-th free id below live.  Counts and
+ * tables follow, and the cache's pages in every layer (cache may be NULL: the
+ * caller moves them).
+ *   moved [pages] int32, out: the new id of every page, -1 for a free one.
+ */
+pi_status pi_pages_compact(const pi_page_state* state, const pi_kv_cache* cache, int32_t* moved,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Page dst[i] = page src[i] in every layer, k and v, i < n (device int32 lists).
+ * Pairs with an id outside 0..pages-1 are ignored.  No page may be in dst twice
+ * or in both lists. */
+pi_status pi_pages_copy(const pi_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                        int32_t n, void* stream);
+
 /* Kernel ids for the timing hooks below. */
 enum {
     PI_K_PRED_L1 = 0,     /* predictor first layer */
@@ -467,7 +673,12 @@ enum {
     PI_K_ACCUMULATE = 11, /* online activation counts from a mask */
     PI_K_STREAM = 12,     /* plain read stream (attainable bandwidth) */
     PI_K_UP_FINISH = 13,  /* sum of the up kernel's K slices + activation (batch >= 2) */
-    PI_K_COUNT = 14
+    PI_K_ROPE_APPEND = 14, /* turned q; turned k and v into the cache */
+    PI_K_ATTN = 15,       /* attention over the cache (all forms) */
+    PI_K_ATTN_JOIN = 16,  /* join of a row's splits */
+    PI_K_PAGES = 17,      /* page bookkeeping */
+    PI_K_PAGE_COPY = 18,  /* page copies and moves */
+    PI_K_COUNT = 19
 };
 
 /*

@@ -22,9 +22,12 @@ PI_RELU, PI_REGLU, PI_SQRELU = 0, 1, 2
 PI_MAX_BATCH = 64
 (PI_K_PRED_L1, PI_K_PRED_L2, PI_K_COMPACT, PI_K_UP, PI_K_DOWN, PI_K_MERGE, PI_K_PROFILE,
  PI_K_INDEX, PI_K_COPY, PI_K_REDUCE, PI_K_FFN, PI_K_ACCUMULATE, PI_K_STREAM, PI_K_UP_FINISH,
- PI_K_COUNT) = range(15)
+ PI_K_ROPE_APPEND, PI_K_ATTN, PI_K_ATTN_JOIN, PI_K_PAGES, PI_K_PAGE_COPY, PI_K_COUNT) = range(20)
 PI_STREAM_SINK_WORDS = 2048
 PI_SCRATCH_BYTES = 32 << 20
+PI_MAX_HEAD_DIM, PI_MAX_PAGE_SIZE = 256, 1024
+PI_ROPE_HALVES, PI_ROPE_PAIRS = 0, 1
+PI_SCALE_NONE, PI_SCALE_LINEAR, PI_SCALE_BASE, PI_SCALE_BANDS = range(4)
 
 # every symbol include/pi.h declares
 EXPORTS = ("pi_workspace_bytes", "pi_workspace_init", "pi_predict", "pi_compact_active",
@@ -36,6 +39,9 @@ EXPORTS = ("pi_workspace_bytes", "pi_workspace_init", "pi_predict", "pi_compact_
            "pi_host_sparse_ffn", "pi_hybrid_host_bytes", "pi_sparse_ffn_hybrid",
            "pi_accumulate_mask", "pi_permute_rows",
            "pi_copy", "pi_stream_read",
+           "pi_rope_turns", "pi_rope_append", "pi_attention_workspace_bytes",
+           "pi_paged_attention", "pi_pages_workspace_bytes", "pi_pages_extend", "pi_pages_fork",
+           "pi_pages_free", "pi_pages_compact", "pi_pages_copy",
            "pi_kernel_timer_start", "pi_kernel_timer_stop", "pi_kernel_name", "pi_status_string",
            "pi_last_error")
 
@@ -66,6 +72,38 @@ class FfnPart(C.Structure):
 class ActiveLists(C.Structure):
     _fields_ = [("n_hot", C.c_int32), ("hot_idx", C.c_void_p), ("cold_idx", C.c_void_p),
                 ("counts", C.c_void_p)]
+
+
+class KvCache(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("layers", C.c_int32), ("pages", C.c_int32),
+                ("kv_heads", C.c_int32), ("page_size", C.c_int32), ("head_dim", C.c_int32),
+                ("k", C.c_void_p), ("v", C.c_void_p)]
+
+
+class SeqBatch(C.Structure):
+    _fields_ = [("n_seqs", C.c_int32), ("n_tokens", C.c_int32), ("max_new", C.c_int32),
+                ("max_len", C.c_int32), ("q_start", C.c_void_p), ("kv_len", C.c_void_p),
+                ("table", C.c_void_p), ("table_stride", C.c_int32)]
+
+
+class Rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class Rope(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int32), ("layout", C.c_int32), ("turns", C.c_void_p),
+                ("magnitude", C.c_float)]
+
+
+class ScoreRule(C.Structure):
+    _fields_ = [("scale", C.c_float), ("cap", C.c_float), ("window", C.c_int32),
+                ("slopes", C.c_void_p), ("prefix", C.c_void_p), ("first", C.c_void_p)]
+
+
+class PageState(C.Structure):
+    _fields_ = [("pages", C.c_int32), ("max_seqs", C.c_int32), ("table_stride", C.c_int32),
+                ("page_size", C.c_int32), ("refs", C.c_void_p), ("table", C.c_void_p),
+                ("lens", C.c_void_p)]
 
 
 _lib = None
@@ -105,6 +143,17 @@ def lib() -> C.CDLL:
         "pi_permute_rows": ([P, P, P, I32, I64, P], I32),
         "pi_copy": ([P, P, I64, P], I32),
         "pi_stream_read": ([P, I64, P, P], I32),
+        "pi_rope_turns": ([I32, C.c_double, I32, C.c_double, C.c_double, C.c_double, C.c_double, P],
+                          I32),
+        "pi_rope_append": ([P, I32, P, P, P, I32, P, P, P, P, P], I32),
+        "pi_attention_workspace_bytes": ([P, P, I32], SZ),
+        "pi_paged_attention": ([P, I32, P, P, I32, P, P, P, P, SZ, P], I32),
+        "pi_pages_workspace_bytes": ([P, I32], SZ),
+        "pi_pages_extend": ([P, P, P, P, I32, P, P, P, SZ, P], I32),
+        "pi_pages_fork": ([P, P, P, I32, P, SZ, P], I32),
+        "pi_pages_free": ([P, P, I32, P], I32),
+        "pi_pages_compact": ([P, P, P, P, SZ, P], I32),
+        "pi_pages_copy": ([P, P, P, I32, P], I32),
         "pi_kernel_timer_start": ([I32, I32], I32),
         "pi_kernel_timer_stop": ([I32, P, P], I32),
         "pi_kernel_name": ([I32], C.c_char_p),
@@ -306,6 +355,77 @@ def pi_stream_read(src, nbytes: int, sink, stream=None):
     _check(lib().pi_stream_read(ptr(src), nbytes, ptr(sink), stream_handle(stream)))
 
 
+# ---- paged key/value cache and the attention over it ----------------------------
+
+def pi_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: int = PI_SCALE_NONE,
+                  factor: float = 1.0, low: float = 1.0, high: float = 4.0, context: float = 0.0):
+    """Turns per position of each pair (float64 CPU tensor; copy it to the device for make_rope)."""
+    import torch
+    turns = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float64)
+    _check(lib().pi_rope_turns(rotary_dim, base, scaling, factor, low, high, context,
+                               turns.data_ptr() or None))
+    return turns
+
+
+def pi_rope_append(cache: KvCache, layer: int, batch: SeqBatch, rope: Rope, q, q_out, k, v,
+                   positions=None, stream=None):
+    """q, q_out [tokens][q_heads][head_dim] (both None: keys and values only), k and v
+    [tokens][kv_heads][head_dim]; the elements of a head contiguous, other strides free."""
+    hq = 0 if q is None else q.shape[1]
+    _check(lib().pi_rope_append(
+        C.byref(cache), layer, C.byref(batch), C.byref(rope), ptr(positions), hq,
+        None if q is None else C.byref(_rows(q, cache, batch, hq)),
+        None if q_out is None else C.byref(_rows(q_out, cache, batch, hq)),
+        C.byref(_rows(k, cache, batch, cache.kv_heads)),
+        C.byref(_rows(v, cache, batch, cache.kv_heads)), stream_handle(stream)))
+
+
+def pi_attention_workspace_bytes(cache: KvCache, batch: SeqBatch, q_heads: int) -> int:
+    return int(lib().pi_attention_workspace_bytes(C.byref(cache), C.byref(batch), q_heads))
+
+
+def pi_paged_attention(cache: KvCache, layer: int, batch: SeqBatch, rule: ScoreRule, q, out,
+                       lse=None, ws=None, stream=None):
+    """q and out [tokens][q_heads][head_dim], lse [tokens][q_heads] float32 or None."""
+    hq = q.shape[1]
+    _check(lib().pi_paged_attention(
+        C.byref(cache), layer, C.byref(batch), C.byref(rule), hq,
+        C.byref(_rows(q, cache, batch, hq)), C.byref(_rows(out, cache, batch, hq)), ptr(lse),
+        ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
+
+
+def pi_pages_workspace_bytes(state: PageState, n: int) -> int:
+    return int(lib().pi_pages_workspace_bytes(C.byref(state), n))
+
+
+def pi_pages_extend(state: PageState, cache: Optional[KvCache], seqs, add, granted, copies, ws,
+                    stream=None):
+    """seqs, add, granted: int32 [n]; copies: int32 [2][n]."""
+    _check(lib().pi_pages_extend(C.byref(state), None if cache is None else C.byref(cache),
+                                 ptr(seqs), ptr(add), seqs.numel(), ptr(granted), ptr(copies),
+                                 ptr(ws), ws.numel() * ws.element_size(), stream_handle(stream)))
+
+
+def pi_pages_fork(state: PageState, src, dst, ws, stream=None):
+    _check(lib().pi_pages_fork(C.byref(state), ptr(src), ptr(dst), src.numel(), ptr(ws),
+                               ws.numel() * ws.element_size(), stream_handle(stream)))
+
+
+def pi_pages_free(state: PageState, seqs, stream=None):
+    _check(lib().pi_pages_free(C.byref(state), ptr(seqs), seqs.numel(), stream_handle(stream)))
+
+
+def pi_pages_compact(state: PageState, cache: Optional[KvCache], moved, ws, stream=None):
+    _check(lib().pi_pages_compact(C.byref(state), None if cache is None else C.byref(cache),
+                                  ptr(moved), ptr(ws), ws.numel() * ws.element_size(),
+                                  stream_handle(stream)))
+
+
+def pi_pages_copy(cache: KvCache, src, dst, stream=None):
+    _check(lib().pi_pages_copy(C.byref(cache), ptr(src), ptr(dst), src.numel(),
+                               stream_handle(stream)))
+
+
 def pi_kernel_timer_start(kid: int, max_launches: int):
     _check(lib().pi_kernel_timer_start(kid, max_launches))
 
@@ -344,6 +464,71 @@ def make_lists(n_hot: int, hot_idx, cold_idx, counts) -> ActiveLists:
     L = ActiveLists(n_hot, ptr(hot_idx), ptr(cold_idx), ptr(counts))
     L._keep = (hot_idx, cold_idx, counts)
     return L
+
+
+def make_kv_cache(k, v) -> KvCache:
+    """k and v: [layers][pages][kv_heads][page_size][head_dim] device tensors."""
+    if k.shape != v.shape or k.dtype != v.dtype or not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k and v must be contiguous and alike in shape and dtype")
+    layers, pages, heads, page_size, head_dim = k.shape
+    c = KvCache(dtype_code(k), layers, pages, heads, page_size, head_dim, ptr(k), ptr(v))
+    c._keep = (k, v)
+    return c
+
+
+def make_seq_batch(q_start, kv_len, table, n_tokens: int, max_new: int, max_len: int) -> SeqBatch:
+    """q_start int32 [n_seqs + 1], kv_len int32 [n_seqs], table int32 [n_seqs][table_stride]."""
+    n = kv_len.numel()
+    _int32("q_start", q_start, (n + 1,))
+    _int32("kv_len", kv_len, (n,))
+    _int32("table", table, (n, table.shape[-1]))
+    b = SeqBatch(n, n_tokens, max_new, max_len, ptr(q_start), ptr(kv_len), ptr(table),
+                 table.shape[-1])
+    b._keep = (q_start, kv_len, table)
+    return b
+
+
+def make_score_rule(scale: float, cap: float = 0.0, slopes=None, window: int = 0, prefix=None,
+                    first=None) -> ScoreRule:
+    """slopes float32 [q_heads], prefix int32 [n_seqs], first int32 [n_tokens] (device) or None."""
+    r = ScoreRule(float(scale), float(cap), int(window), ptr(slopes), ptr(prefix), ptr(first))
+    r._keep = (slopes, prefix, first)
+    return r
+
+
+def make_rope(turns, pairs: bool = False, magnitude: float = 1.0) -> Rope:
+    """turns: float64 device tensor [rotary_dim / 2] (pi_rope_turns)."""
+    r = Rope(2 * turns.numel(), PI_ROPE_PAIRS if pairs else PI_ROPE_HALVES, ptr(turns) or None,
+             float(magnitude))
+    r._keep = turns
+    return r
+
+
+def make_page_state(refs, table, lens, page_size: int) -> PageState:
+    """refs int32 [pages], table int32 [max_seqs][table_stride], lens int32 [max_seqs]."""
+    n = lens.numel()
+    _int32("refs", refs, (refs.numel(),))
+    _int32("table", table, (n, table.shape[-1]))
+    _int32("lens", lens, (n,))
+    s = PageState(refs.numel(), n, table.shape[-1], page_size, ptr(refs), ptr(table), ptr(lens))
+    s._keep = (refs, table, lens)
+    return s
+
+
+def _int32(name: str, t, shape):
+    if str(t.dtype) != "torch.int32" or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _rows(t, cache: KvCache, batch: SeqBatch, heads: int) -> Rows:
+    """[tokens][heads][head_dim] as the library sees it; the shape is checked here, where it is known."""
+    if t.dim() != 3 or t.shape[0] < batch.n_tokens or t.shape[1] != heads or \
+            t.shape[2] != cache.head_dim or t.stride(2) != 1:
+        raise ValueError(f"need [{batch.n_tokens}][{heads}][{cache.head_dim}] with contiguous heads, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+    if dtype_code(t) != cache.dtype:
+        raise TypeError("q, k, v and the output have the cache's dtype")
+    return Rows(ptr(t), t.stride(0), t.stride(1))
 
 
 def row_slice(t, lo: int, hi: int):

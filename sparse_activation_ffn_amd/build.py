@@ -8,13 +8,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpi.so")
-SOURCES = [os.path.join(CSRC, "pi_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("pi_api.hip", "pi_attn.hip", "pi_pages.hip")]
 # host-core code of the hybrid step: built by the host compiler, linked in
 HOST_SOURCES = [os.path.join(CSRC, "pi_host.cpp")]
 DEPS = SOURCES + HOST_SOURCES + \
@@ -26,7 +27,7 @@ CXX = os.environ.get("CXX", "g++")
 # AVX2 / F16C / FMA code is selected per function at run time, so the baseline ISA stays generic
 HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-pthread", "-Wall"]
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # packed fp32 instructions stay off: only plain fp32 VALU ops are emitted
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-result",
@@ -40,19 +41,19 @@ def build(force: bool = True, verbose: bool = False) -> str:
         if os.path.getmtime(LIB) >= newest:
             return LIB
     tmp = LIB + ".tmp"
-    objs = []
-    for src in HOST_SOURCES:
-        obj = os.path.join(PKG, os.path.basename(src) + ".tmp.o")
-        cmd = [CXX, *HOST_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
+    jobs = [[CXX, *HOST_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src] for src in HOST_SOURCES] + \
+        [[HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src] for src in SOURCES]
+    objs = [os.path.join(PKG, os.path.basename(cmd[-1]) + ".tmp.o") for cmd in jobs]
+
+    def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
-    cmd = [HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, *SOURCES, "-x", "none", *objs, "-pthread", "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
+
     try:
-        subprocess.run(cmd, check=True)
+        with ThreadPoolExecutor(max_workers=len(jobs)) as pool:     # the sources side by side
+            list(pool.map(run, [[*cmd, "-o", obj] for cmd, obj in zip(jobs, objs)]))
+        run([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-pthread", "-o", tmp])
     finally:
         for obj in objs:
             if os.path.exists(obj):

@@ -16,6 +16,7 @@
 #include "pi_ffn.h"
 #include "pi_host.h"
 #include "pi_kernels.h"
+#include "pi_launch.h"
 #include "pi_mfma.h"
 
 using namespace pi;
@@ -25,9 +26,11 @@ using namespace pi;
 // stand-in; the device address comes from hipGetSymbolAddress (scratch_ptr).
 static __device__ __align__(256) uint8_t scratch[PI_SCRATCH_BYTES];
 
-namespace {
+// ---- shared by the library's translation units (pi_launch.h) --------------------
+namespace pi {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
+static thread_local Timer g_timers[PI_K_COUNT];
 
 pi_status fail(pi_status s, const char* fmt, ...) {
     va_list ap;
@@ -37,12 +40,11 @@ pi_status fail(pi_status s, const char* fmt, ...) {
     return s;
 }
 
-#define CHECK(cond, status, ...)                          \
-    do {                                                  \
-        if (!(cond)) return fail(status, __VA_ARGS__);    \
-    } while (0)
+Timer& kernel_timer(int kid) { return g_timers[kid]; }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace pi
+
+namespace {
 
 // ---- workspace layout -------------------------------------------------------
 // [0, 256)     reserved header
@@ -170,31 +172,6 @@ size_t ws_ffn_bytes(int d, int n, int B, int nparts) {
     return WS_CTR_BYTES + ws_h_bytes(n, B) + ws_part_bytes(d, n, B, nparts);
 }
 
-// ---- timing hooks --------------------------------------------------------------
-struct Timer {
-    bool armed = false;
-    int max = 0, used = 0;
-    std::vector<hipEvent_t> ev;   // 2 per launch
-};
-thread_local Timer g_timers[PI_K_COUNT];
-
-template <typename K, typename... Args>
-pi_status launch(int kid, K kernel, dim3 grid, dim3 block, size_t shmem, hipStream_t s,
-                 Args... args) {
-    Timer& t = g_timers[kid];
-    if (t.armed && t.used < t.max) {
-        hipExtLaunchKernelGGL(kernel, grid, block, (uint32_t)shmem, s, t.ev[2 * t.used],
-                              t.ev[2 * t.used + 1], 0, args...);
-        ++t.used;
-    } else {
-        hipLaunchKernelGGL(kernel, grid, block, shmem, s, args...);
-    }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return fail(PI_ERR_HIP, "%s launch: %s", pi_kernel_name(kid), hipGetErrorString(e));
-    return PI_OK;
-}
-
 // ---- static scratch of the no-allocation entry point ------------------------------
 // `scratch` (file scope, below the includes): one copy per GPU, held until the
 // process ends.  Host code never uses the array's name as an address: the device
@@ -318,12 +295,6 @@ pi_status check_ws(void* ws, size_t have, size_t need) {
     CHECK(have >= need, PI_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
     return PI_OK;
 }
-
-#define TRY(expr)                         \
-    do {                                  \
-        pi_status _s = (expr);            \
-        if (_s != PI_OK) return _s;       \
-    } while (0)
 
 // ---- template dispatch ---------------------------------------------------------
 // kernels with more than 64 KiB of dynamic LDS must opt in
@@ -721,7 +692,8 @@ const char* pi_kernel_name(int32_t kid) {
     static const char* names[PI_K_COUNT] = {"k_pred_l1", "k_pred_l2", "k_compact", "k_up", "k_down",
                                             "k_merge", "k_profile", "k_index", "k_copy", "k_reduce",
                                             "k_ffn", "k_accumulate_mask", "k_stream_read",
-                                            "k_up_finish"};
+                                            "k_up_finish", "k_rope_append", "k_attn", "k_attn_join", "k_pages",
+                                            "k_page_copy"};
     return (kid >= 0 && kid < PI_K_COUNT) ? names[kid] : "?";
 }
 
