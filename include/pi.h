@@ -492,7 +492,7 @@ typedef struct pi_seq_batch {
     const int32_t* q_start; /* [n_seqs + 1] device, ascending */
     const int32_t* kv_len;  /* [n_seqs] device: tokens in the cache, the new ones included */
     const int32_t* table;   /* [n_seqs][table_stride] device: page ids */
-    int32_t table_stride;   /* >= 1; a sequence is at most table_stride * page_size tokens long */
+    int32_t table_stride;   /* >= 1; a sequence is at most table_stride * page_size tokens long, and 2^30 */
 } pi_seq_batch;
 
 /* One [n_tokens][heads][head_dim] tensor with strides in elements; the

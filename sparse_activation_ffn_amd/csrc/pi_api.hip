@@ -297,16 +297,6 @@ pi_status check_ws(void* ws, size_t have, size_t need) {
 }
 
 // ---- template dispatch ---------------------------------------------------------
-// kernels with more than 64 KiB of dynamic LDS must opt in
-template <typename K>
-pi_status allow_lds(K kernel, size_t bytes) {
-    if (bytes <= 65536) return PI_OK;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != hipSuccess) return fail(PI_ERR_HIP, "LDS attribute: %s", hipGetErrorString(e));
-    return PI_OK;
-}
-
 template <int WT, int XT, int BT>
 pi_status launch_pred_l1(const pi_predictor* p, const void* x, int B, float* u, hipStream_t s) {
     return launch(PI_K_PRED_L1, k_pred_l1<WT, XT, BT>, dim3(p->r), dim3(THREADS), 0, s,

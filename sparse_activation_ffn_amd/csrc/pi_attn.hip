@@ -5,31 +5,12 @@
 #include <cmath>
 
 #include "pi.h"
-#include "pi_cache.h"
+#include "pi_attn.h"
 #include "pi_launch.h"
 
 using namespace pi;
 
 namespace {
-
-struct AttnArgs {
-    CacheLayer c;
-    Batch b;
-    const uint8_t* q;
-    uint8_t* out;
-    float* lse;
-    int64_t q_ts, q_hs, o_ts, o_hs;
-    int q_heads, group;
-    float scale, cap;
-    int window;
-    const float* slopes;
-    const int* prefix;
-    const int* first;
-};
-
-template <int DT> struct ElemT;
-template <> struct ElemT<F32> { typedef float T; };
-template <> struct ElemT<F16> { typedef _Float16 T; };
 
 constexpr int MAXD_PER_LANE = PI_MAX_HEAD_DIM / WAVE;
 
@@ -97,6 +78,62 @@ __global__ __launch_bounds__(WAVE) void k_attn(AttnArgs a) {
     if (a.lse && lane == 0) a.lse[(int64_t)t * a.q_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Which kernel a call runs, how the keys are split, and the workspace for it.
+struct Plan {
+    bool few;                  // at most 16 rows per sequence and key head
+    int rows, chunk, splits;
+    size_t part, ml, n, bytes; // offsets in the workspace, its size
+};
+
+Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
+    Plan p{};
+    const int64_t rows = (int64_t)std::min(b->max_new, b->n_tokens) * (q_heads / c->kv_heads);
+    p.few = rows <= FEW_ROWS;
+    p.rows = (int)std::min<int64_t>(rows, FEW_ROWS);
+    p.splits = 1;
+    p.chunk = 1 << 30;
+    if (p.few) {
+        const int64_t alone = std::max<int64_t>(1, (int64_t)b->n_seqs * c->kv_heads);
+        const int64_t want = std::max<int64_t>(1, 2048 / alone);
+        const int64_t chunk = std::max<int64_t>(256, ((int64_t)b->max_len + want - 1) / want);
+        p.chunk = (int)std::min<int64_t>((chunk + 127) / 128 * 128, 1 << 30);
+        p.splits = std::max(1, (int)(((int64_t)b->max_len + p.chunk - 1) / p.chunk));
+    }
+    p.part = 0;
+    const size_t slots = p.splits > 1 ? (size_t)b->n_seqs * c->kv_heads * p.splits * p.rows : 0;
+    p.ml = align256(slots * c->head_dim * 4);
+    p.n = p.ml + align256(slots * 8);
+    p.bytes = p.n + align256(std::max<size_t>((size_t)b->n_seqs * 4, 4));
+    return p;
+}
+
+template <int DT, int DP, bool FULL>
+pi_status launch_few(const AttnArgs& a, hipStream_t s) {
+    auto kern = k_attn_few<DT, DP, FULL>;
+    TRY(allow_lds(kern, few_lds<DP>()));
+    TRY(launch(PI_K_ATTN, kern, dim3(a.splits, a.c.kv_heads, a.b.n_seqs), dim3(WAVE * FEW_WAVES), few_lds<DP>(), s, a));
+    if (a.splits == 1) return PI_OK;
+    const int pieces = a.rows * (a.c.head_dim / 4);
+    return launch(PI_K_ATTN_JOIN, k_attn_join<DT>, dim3((pieces + WAVE - 1) / WAVE, a.c.kv_heads, a.b.n_seqs), dim3(WAVE),
+                  0, s, a);
+}
+
+template <int DT>
+pi_status attend(const AttnArgs& a, const Plan& p, int q_heads, hipStream_t s) {
+    const int d = a.c.head_dim;
+    if (p.few) {
+        if (d == 64) return launch_few<DT, 64, true>(a, s);
+        if (d < 64) return launch_few<DT, 64, false>(a, s);
+        if (d == 128) return launch_few<DT, 128, true>(a, s);
+        if (d < 128) return launch_few<DT, 128, false>(a, s);
+        if (d == 256) return launch_few<DT, 256, true>(a, s);
+        return launch_few<DT, 256, false>(a, s);
+    }
+    return launch(PI_K_ATTN, k_attn<DT>, dim3(a.b.n_tokens, q_heads), dim3(WAVE), 0, s, a);
+}
+
 pi_status check_q_heads(const pi_kv_cache* c, int q_heads) {
     CHECK(q_heads >= 1 && q_heads <= 65535 && q_heads % c->kv_heads == 0, PI_ERR_SHAPE,
           "q_heads (%d) must be a multiple of kv_heads (%d) and at most 65535", q_heads, c->kv_heads);
@@ -109,7 +146,7 @@ extern "C" {
 
 size_t pi_attention_workspace_bytes(const pi_kv_cache* cache, const pi_seq_batch* batch, int32_t q_heads) {
     if (check_cache(cache) != PI_OK || check_batch(batch) != PI_OK || check_q_heads(cache, q_heads) != PI_OK) return 0;
-    return 256;
+    return plan_attention(cache, batch, q_heads).bytes;
 }
 
 pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_seq_batch* batch,
@@ -126,10 +163,11 @@ pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_s
     if (batch->n_seqs == 0 || batch->n_tokens == 0) return PI_OK;
     TRY(check_rows(q, "q", cache->dtype));
     TRY(check_rows(out, "out", cache->dtype));
-    const size_t need = pi_attention_workspace_bytes(cache, batch, q_heads);
+    const Plan p = plan_attention(cache, batch, q_heads);
     CHECK(ws, PI_ERR_WORKSPACE, "workspace is NULL");
     CHECK(aligned(ws, 256), PI_ERR_ALIGN, "workspace must be 256-byte aligned");
-    CHECK(ws_bytes >= need, PI_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    CHECK(ws_bytes >= p.bytes, PI_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p.bytes);
+    if (batch->max_new == 0) return PI_OK;
     AttnArgs a{};
     a.c = cache_layer(cache, layer);
     a.b = seq_batch(batch);
@@ -148,9 +186,14 @@ pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_s
     a.slopes = rule->slopes;
     a.prefix = rule->prefix;
     a.first = rule->first;
-    const dim3 grid(batch->n_tokens, q_heads);
-    return cache->dtype == PI_F32 ? launch(PI_K_ATTN, k_attn<F32>, grid, dim3(WAVE), 0, (hipStream_t)stream, a)
-                                  : launch(PI_K_ATTN, k_attn<F16>, grid, dim3(WAVE), 0, (hipStream_t)stream, a);
+    a.rows = p.rows;
+    a.chunk = p.chunk;
+    a.splits = p.splits;
+    a.part = (float*)((uint8_t*)ws + p.part);
+    a.part_ml = (float2*)((uint8_t*)ws + p.ml);
+    a.part_n = (int*)((uint8_t*)ws + p.n);
+    hipStream_t s = (hipStream_t)stream;
+    return cache->dtype == PI_F32 ? attend<F32>(a, p, q_heads, s) : attend<F16>(a, p, q_heads, s);
 }
 
 }  // extern "C"

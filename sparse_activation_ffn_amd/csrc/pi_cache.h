@@ -94,9 +94,9 @@ inline pi_status check_rows(const pi_rows* r, const char* name, int dtype) {
 
 // ---- device ---------------------------------------------------------------------
 
-// tokens of sequence s that its table can hold
+// tokens of sequence s that its table can hold (and 2^30 at most: sums of two stay in 32 bits)
 __device__ __forceinline__ int clamped_len(const Batch& b, const int page_shift, int s) {
-    const int64_t cap = (int64_t)b.table_stride << page_shift;
+    const int64_t cap = min((int64_t)b.table_stride << page_shift, (int64_t)1 << 30);
     const int len = b.kv_len[s];
     return len < 0 ? 0 : len > cap ? (int)cap : len;
 }

@@ -52,4 +52,14 @@ pi_status launch(int kid, K kernel, dim3 grid, dim3 block, size_t shmem, hipStre
     return PI_OK;
 }
 
+// kernels with more than 64 KiB of dynamic LDS must opt in
+template <typename K>
+pi_status allow_lds(K kernel, size_t bytes) {
+    if (bytes <= 65536) return PI_OK;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != hipSuccess) return fail(PI_ERR_HIP, "LDS attribute: %s", hipGetErrorString(e));
+    return PI_OK;
+}
+
 }  // namespace pi
