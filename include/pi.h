@@ -485,7 +485,7 @@ typedef struct pi_kv_cache {
  * q_start[s+1] and is its token at position kv_len[s] - (q_start[s+1] - t).
  * Rows that belong to no sequence are left as they are. */
 typedef struct pi_seq_batch {
-    int32_t n_seqs;         /* 0..2^20 */
+    int32_t n_seqs;         /* 0..65535 */
     int32_t n_tokens;       /* rows of q, 0..2^23 */
     int32_t max_new;        /* most new tokens of one sequence; rows beyond it are not computed */
     int32_t max_len;        /* most tokens of one sequence (a hint for the split of the work) */

@@ -24,6 +24,7 @@ constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float SLACK = 8.0f;
 constexpr float LIFT = 6.0f;
+constexpr int XCDS = 8;               // dies with an L2 each; workgroups go round them
 
 struct AttnArgs {
     CacheLayer c;
@@ -40,10 +41,12 @@ struct AttnArgs {
     const int* first;
     // split of the keys
     int chunk, splits;                // keys per split, most splits of a sequence
-    int rows;                         // rows per sequence and key head that the workspace holds
-    float* part;                      // [n_seqs][kv_heads][splits][rows][head_dim], when splits > 1
-    float2* part_ml;                  // [n_seqs][kv_heads][splits][rows]: reference, sum
-    int* part_n;                      // [n_seqs]: splits that hold something
+    int tiles;                        // row tiles of the call (few rows: one per sequence)
+    int rows;                         // rows of a tile
+    int64_t most_rows;                // rows of a sequence and key head that are computed
+    float* part;                      // [tiles][kv_heads][splits][rows][head_dim], when splits > 1
+    float2* part_ml;                  // [tiles][kv_heads][splits][rows]: reference, sum
+    int* part_n;                      // [tiles]: splits that hold something
 };
 
 // keys that row t at position pos of sequence s sees
@@ -62,6 +65,14 @@ __device__ __forceinline__ float weight_of(float m, float top) {
 
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - LIFT + __builtin_amdgcn_logf(l)) * LN2;
+}
+
+// tanh for the cap on scores.  1 - 2 / (e^2y + 1) is within 2^-22 of it (absolute); for 32-bit caches the
+// library's, whose relative error is that small
+template <int DT>
+__device__ __forceinline__ float tanh_of(float y) {
+    if (DT == F32) return tanhf(y);
+    return 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * LOG2E * y) + 1.0f);
 }
 
 template <int DT> struct ElemT;
@@ -287,7 +298,7 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
             for (int i = 0; i < 4; ++i) {
                 const int key = j + 16 * u + 4 * g + i;
                 float v = sc[u][i] * scale;
-                if (a.cap > 0.0f) v = a.cap * LOG2E * tanhf(v);
+                if (a.cap > 0.0f) v = a.cap * LOG2E * tanh_of<DT>(v);
                 if (a.slopes) v -= slope * (float)abs(pos - key);
                 sees[u][i] = true;
                 if (!whole) {
@@ -471,16 +482,450 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
     }
 }
 
+// ---- many rows: chunks of new tokens -----------------------------------------------
+//
+// Bound by the matrix cores, so the loads serve them: a workgroup takes MANY_ROWS
+// rows (row r of a sequence and key head: token r / group, so all query heads of
+// a key head share its keys) and walks over the keys in tiles of TILE.  The tile
+// after the current one is on its way from memory to LDS meanwhile (two buffers,
+// loads that write LDS directly).  Each wave owns 32 rows:
+//   S^T = K Q^T (32 keys x 32 rows per instruction): the queries stay in
+//   registers; lane (m = lane % 32, h = lane / 32) gets the scores of row m with the
+//   keys 8b + 4h + i of a block of 32, i < 4;
+//   O^T = V^T P^T: these weights are the B operand as they lie, if the sum over
+//   the keys is taken in that order; the A operand is V read from LDS
+//   transposed (f16) or as it lies (f32: elements c, c + DP / 32, ... make a tile).
+// LDS rows are DP elements without padding; the 16-byte pieces of row r are
+// permuted by an exclusive or with a function of r, chosen so that the rows that
+// one instruction reads lie in different banks.
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+
+constexpr int MANY_WAVES = 4;
+constexpr int MANY_ROWS = 32 * MANY_WAVES;
+
+template <int DT, int DP> struct Many {
+    static constexpr int TILE = DT == F16 && DP <= 128 ? 64 : 32;   // keys per tile
+    static constexpr int ES = DT == F16 ? 2 : 4;
+    static constexpr int ROW = DP * ES;                             // bytes of an LDS row
+    static constexpr int BYTES = TILE * ROW;
+};
+
+template <int DT, int DP> constexpr size_t many_lds() { return 4 * Many<DT, DP>::BYTES; }   // K, V, twice
+
+// piece c of row r of a K tile: 16 rows in a row at the same c read 16 different pieces of 256 bytes
+template <int ROW>
+__device__ __forceinline__ int k_piece(int r, int c) {
+    return c ^ (ROW >= 256 ? r & 15 : (r >> 1) & 7);
+}
+// of a V tile, f16: 4 rows at 4 pieces each (a transposed read) are 16 different pieces of 256 bytes;
+// f32: a read takes whole rows, two of them 4 apart
+template <int DT, int ROW>
+__device__ __forceinline__ int v_piece(int r, int c) {
+    if (DT == F32) return c;
+    return c ^ (ROW >= 256 ? (r & 3) << 2 : ((r >> 1) & 1) << 2);
+}
+
+__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// all loads of this wave have arrived (vmcnt 0, the other counters as they are)
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// The sequence and first row of row tile `flat` when sequences have tiles of `tile`
+// rows, at most `most` rows each; false past the last one.  The whole wave calls it.
+__device__ __forceinline__ bool tile_at(const AttnArgs& a, int flat, int tile, int64_t most, int& s, int& r0) {
+    const int lane = threadIdx.x % WAVE;
+    int before = 0;
+    for (int base = 0; base < a.b.n_seqs; base += WAVE) {
+        int n = 0;
+        if (base + lane < a.b.n_seqs) {
+            const int t0 = max(a.b.q_start[base + lane], 0), t1 = min(a.b.q_start[base + lane + 1], a.b.n_tokens);
+            n = (int)((min(max((int64_t)t1 - t0, (int64_t)0) * a.group, most) + tile - 1) / tile);
+        }
+        const int incl = wave_incl_scan(n);
+        const uint64_t past = __ballot(before + incl > flat);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            s = base + at;
+            r0 = (flat - before - (__shfl(incl, at, WAVE) - __shfl(n, at, WAVE))) * tile;
+            return true;
+        }
+        before += __shfl(incl, WAVE - 1, WAVE);
+    }
+    return false;
+}
+
+__device__ __forceinline__ bool finite(float f) { return f - f == 0.0f; }
+
+// output element of acc[t][i] in lane half h
+template <int DT, int DP>
+__device__ __forceinline__ int out_elem(int t, int i, int h) {
+    const int r = 8 * (i / 4) + 4 * h + i % 4;
+    return DT == F16 ? 32 * t + r : DP / 32 * r + t;
+}
+
+// Where some row of the wave does not see every key of a tile, an infinity or NaN in V would reach it through
+// 0 * V.  Such elements are left out of the product, and added here to the rows that see them: of keys
+// k0 <= k < k1 of the tile with a page (ok), each lane's row sees lo <= k < hi.
+template <int DT, int DP>
+__device__ __forceinline__ void add_nonfinite(f16v* acc, const uint8_t* vt, int lane, int k0, int k1, int lo, int hi,
+                                              uint64_t ok) {
+    constexpr int ES = Many<DT, DP>::ES, ROW = Many<DT, DP>::ROW, ND = DP / 32, EV = 16 / ES;
+    for (int k = k0; k < k1; ++k) {
+        if (!((ok >> k) & 1)) continue;
+        bool odd = false;
+        for (int i = lane; i < ROW / 4; i += WAVE) {
+            const unsigned w = *reinterpret_cast<const unsigned*>(vt + k * ROW + i * 4);
+            odd |= DT == F16 ? nonfinite_h2(w) != 0 : !finite(bits_f(w));
+        }
+        if (!__any(odd)) continue;
+        const bool sees = k >= lo && k < hi;
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int e = out_elem<DT, DP>(t, i, lane / 32);
+                const uint8_t* p = vt + k * ROW + v_piece<DT, ROW>(k, e / EV) * 16 + (e % EV) * ES;
+                const float f = DT == F16 ? half_f(*reinterpret_cast<const uint16_t*>(p)) : *reinterpret_cast<const float*>(p);
+                acc[t][i] += sees && !finite(f) ? f : 0.0f;
+            }
+    }
+}
+
+// RULES: scores may be capped or biased (else they are scale * q.k alone)
+template <int DT, int DP, bool FULL, bool RULES>
+__global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a) {
+    typedef Many<DT, DP> M;
+    constexpr int TILE = M::TILE, ES = M::ES, ROW = M::ROW, KB = TILE / 32;
+    constexpr int EV = 16 / ES, NC = ROW / 16;     // elements per piece, pieces per row
+    constexpr int NK = NC / 2;                     // pieces of a key per lane
+    constexpr int ND = DP / 32;                    // tiles of 32 elements of the output
+    constexpr int RPI = 1024 / ROW;                // rows per load instruction
+    constexpr int LOADS = TILE / RPI / MANY_WAVES; // load instructions per wave, K and V each
+    extern __shared__ __align__(1024) uint8_t smem[];
+
+    // work item: row tiles fastest, last (longest) first, and each XCD a run of its own, so that the
+    // workgroups that share keys share an L2
+    const int items = gridDim.x, per = (items + XCDS - 1) / XCDS;
+    const int item = (blockIdx.x % XCDS) * per + blockIdx.x / XCDS;
+    const int total = a.tiles * a.c.kv_heads * a.splits;
+    if (item >= total) return;
+    const int sp = item % a.splits, rest = item / a.splits;
+    const int flat = a.tiles - 1 - rest % a.tiles, kvh = rest / a.tiles;
+    int s, r0;
+    if (!tile_at(a, flat, MANY_ROWS, a.most_rows, s, r0)) return;
+    s = __builtin_amdgcn_readfirstlane(s);
+    r0 = __builtin_amdgcn_readfirstlane(r0);
+
+    const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int m = lane % 32, h = lane / 32;
+    const int d = FULL ? DP : a.c.head_dim;
+    const int ps = a.c.page_size, shift = a.c.page_shift;
+    const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
+    const int len = clamped_len(a.b, shift, s), q_end = a.b.q_start[s + 1];
+    const int n_rows = (int)min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)MANY_ROWS);
+
+    const int my = wave * 32 + m;
+    const bool row = my < n_rows;
+    const int tok = t0 + (r0 + my) / a.group, head = kvh * a.group + (r0 + my) % a.group;
+    int lo = 0, hi = 0, pos = 0;
+    if (row) {
+        pos = len - (q_end - tok);
+        visible(a, tok, pos, s, len, lo, hi);
+    }
+    // keys that some row of the wave sees, keys that all of them see; then the workgroup's
+    int w_lo = lo < hi ? lo : 0x7fffffff, w_hi = lo < hi ? hi : 0, in_lo = row ? lo : 0, in_hi = row ? hi : 0x7fffffff;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        w_lo = min(w_lo, __shfl_xor(w_lo, o, WAVE));
+        w_hi = max(w_hi, __shfl_xor(w_hi, o, WAVE));
+        in_lo = max(in_lo, __shfl_xor(in_lo, o, WAVE));
+        in_hi = min(in_hi, __shfl_xor(in_hi, o, WAVE));
+    }
+    w_lo = __builtin_amdgcn_readfirstlane(w_lo);
+    w_hi = __builtin_amdgcn_readfirstlane(w_hi);
+    in_lo = __builtin_amdgcn_readfirstlane(in_lo);
+    in_hi = __builtin_amdgcn_readfirstlane(in_hi);
+    int* scratch = reinterpret_cast<int*>(smem);
+    if (lane == 0) {
+        scratch[wave] = w_lo;
+        scratch[MANY_WAVES + wave] = w_hi;
+    }
+    __syncthreads();
+    int start = 0x7fffffff, end = 0;
+#pragma unroll
+    for (int w = 0; w < MANY_WAVES; ++w) {
+        start = min(start, scratch[w]);
+        end = max(end, scratch[MANY_WAVES + w]);
+    }
+    __syncthreads();
+    start = __builtin_amdgcn_readfirstlane(end > 0 ? start & ~(TILE - 1) : 0);
+    end = __builtin_amdgcn_readfirstlane(end);
+    const int n_split = active_splits(a, start, end);
+    if (sp >= n_split) return;
+    if (a.splits > 1 && sp == 0 && kvh == 0 && threadIdx.x == 0) a.part_n[flat] = n_split;
+    const int from = start + sp * a.chunk;
+    const int to = sp == n_split - 1 ? end : from + a.chunk;
+
+    // queries: B operand, row m, pieces 2c + h.  A negative scale goes into their sign.
+    u4 q[NK];
+    const unsigned flip = a.scale < 0.0f ? (DT == F16 ? 0x80008000u : 0x80000000u) : 0u;
+#pragma unroll
+    for (int c = 0; c < NK; ++c) {
+        const int e = (2 * c + h) * EV;
+        q[c] = u4{0, 0, 0, 0};
+        if (row && (FULL || e < d)) q[c] = ld16(a.q + (tok * a.q_ts + head * a.q_hs + e) * ES);
+        q[c] ^= flip;
+    }
+    const float abs_scale = fabsf(a.scale);
+    const float scale = RULES && a.cap > 0.0f ? abs_scale / a.cap : abs_scale * LOG2E;
+    const float slope = RULES && a.slopes && row ? a.slopes[head] * LOG2E : 0.0f;
+
+    const int* table = a.b.table + (int64_t)s * a.b.table_stride;
+    const int last_page = max(len - 1, 0) >> shift;
+    const int64_t page_bytes = (int64_t)a.c.kv_heads * ps * d * ES;
+    const int head_off = kvh * ps;
+
+    // pieces past the head's last element are zero, and no load writes them
+    if (!FULL) {
+        for (int i = threadIdx.x; i < 4 * M::BYTES / 16; i += WAVE * MANY_WAVES)
+            reinterpret_cast<u4*>(smem)[i] = u4{0, 0, 0, 0};
+        __syncthreads();
+    }
+    auto page_of = [&](int j) { return table[min((j + lane) >> shift, last_page)]; };
+    // keys j .. j + TILE - 1 into buffer b; `page` holds the page of key j + lane
+    auto load_tile = [&](int j, int page, int b) {
+        uint8_t* kt = smem + b * 2 * M::BYTES;
+        const int safe = (unsigned)page < (unsigned)a.c.pages ? page : 0;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int first = (wave * LOADS + i) * RPI, r = first + lane / NC, at = lane % NC;
+            const int p = __shfl(safe, r, WAVE);
+            const int64_t off = p * page_bytes + (int64_t)(head_off + ((j + r) & (ps - 1))) * d * ES;
+            const int kc = k_piece<ROW>(r, at), vc = v_piece<DT, ROW>(r, at);
+            if (FULL || kc * EV < d) load_to_lds(a.c.k + off + kc * 16, kt + first * ROW);
+            if (FULL || vc * EV < d) load_to_lds(a.c.v + off + vc * 16, kt + M::BYTES + first * ROW);
+        }
+    };
+
+    f16v acc[ND];
+#pragma unroll
+    for (int t = 0; t < ND; ++t) acc[t] = f16v{};
+    float ref = -INFINITY, sum = 0.0f;
+
+    int page = 0, page_next = 0;
+    if (from < to) {
+        page = page_of(from);
+        load_tile(from, page, 0);
+        page_next = page_of(from + TILE);
+    }
+    int b = 0;
+    for (int j = from; j < to; j += TILE, b ^= 1) {
+        wait_loads();
+        __syncthreads();                           // tile j is there, and every wave is done with the other buffer
+        const uint64_t ok = __ballot((unsigned)page < (unsigned)a.c.pages);
+        if (j + TILE < to) {
+            load_tile(j + TILE, page_next, b ^ 1);
+            page = page_next;
+            page_next = page_of(j + 2 * TILE);
+        }
+        if (j >= w_hi || j + TILE <= w_lo) continue;   // no row of this wave sees these keys
+        const uint8_t* kt = smem + b * 2 * M::BYTES;
+        const uint8_t* vt = kt + M::BYTES;
+
+        f16v sc[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            sc[k] = f16v{};
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+                const u4 kk = *reinterpret_cast<const u4*>(kt + (k * 32 + m) * ROW + k_piece<ROW>(k * 32 + m, 2 * c + h) * 16);
+                if constexpr (DT == F16) {
+                    sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kk), __builtin_bit_cast(h8, q[c]),
+                                                                   sc[k], 0, 0, 0);
+                } else {
+                    const f4 kf = __builtin_bit_cast(f4, kk), qf = __builtin_bit_cast(f4, q[c]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(kf[e], qf[e], sc[k], 0, 0, 0);
+                }
+            }
+        }
+        // key of score r of block k: j + 32 k + 8 (r / 4) + 4 h + r % 4
+        constexpr uint64_t ALL = TILE == 64 ? ~0ull : (1ull << (TILE % 64)) - 1;
+        const bool whole = j >= in_lo && j + TILE <= in_hi && j + TILE <= to && (ok & ALL) == ALL;
+        if (RULES) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float v = sc[k][r] * scale;
+                    if (a.cap > 0.0f) v = a.cap * LOG2E * tanh_of<DT>(v);
+                    if (a.slopes) v -= slope * (float)abs(pos - (j + 32 * k + 8 * (r / 4) + 4 * h + r % 4));
+                    sc[k][r] = v;
+                }
+        }
+        auto sees = [&](int k, int r) {
+            const int key = 32 * k + 8 * (r / 4) + 4 * h + r % 4;
+            return j + key >= lo && j + key < hi && j + key < to && ((ok >> key) & 1);
+        };
+        if (!whole) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sc[k][r] = sees(k, r) ? sc[k][r] : -INFINITY;
+        }
+        float top = sc[0][0];
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
+        const float unit = RULES ? 1.0f : scale;
+        top *= unit;
+        if (__any(top > ref + SLACK)) {
+            top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+            const float now = fmaxf(ref, top), f = weight_of(ref, now);
+            ref = now;
+            sum *= f;
+#pragma unroll
+            for (int t = 0; t < ND; ++t) acc[t] *= f;
+        }
+        const float off = LIFT - (ref == -INFINITY ? 0.0f : ref);
+        float part = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                sc[k][r] = __builtin_amdgcn_exp2f(fmaf(sc[k][r], unit, off));
+                part += sc[k][r];
+            }
+        sum += part;
+
+        if constexpr (DT == F16) {
+            h8 p[2 * KB];                          // keys 16 n + {4 h + i, 8 + 4 h + i}
+#pragma unroll
+            for (int n = 0; n < 2 * KB; ++n)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[n][e] = (_Float16)sc[n / 2][8 * (n % 2) + e];
+            // V^T: elements 32 t + m of these keys
+            auto v_at = [&](int t, int n) {
+                const int l = lane % 16, r = 16 * n + 4 * h + l / 4, e = 32 * t + 16 * ((lane / 16) % 2) + 4 * (l % 4);
+                const uint8_t* p0 = vt + r * ROW + v_piece<DT, ROW>(r, e / 8) * 16 + (e % 8) * 2;
+                const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p0);
+                // rows 8 further on: the permutation repeats
+                const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(p0 + 8 * ROW));
+                return __builtin_bit_cast(h8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+            bool special = false;
+            if (!whole) {
+                unsigned odd = 0;
+#pragma unroll 1
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int n = 0; n < 2 * KB; ++n) {
+                        const u4 w = __builtin_bit_cast(u4, v_at(t, n));
+                        odd |= nonfinite_h2(w.x) | nonfinite_h2(w.y) | nonfinite_h2(w.z) | nonfinite_h2(w.w);
+                    }
+                special = __any(odd != 0);
+            }
+            if (!special) {
+#pragma unroll
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int n = 0; n < 2 * KB; ++n)
+                        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_at(t, n), p[n], acc[t], 0, 0, 0);
+            } else {
+                add_nonfinite<DT, DP>(acc, vt, lane, max(w_lo - j, 0), min(min(w_hi, to) - j, TILE), lo - j, hi - j, ok);
+#pragma unroll
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int n = 0; n < 2 * KB; ++n) {
+                        h8 v = v_at(t, n);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = finite((float)v[e]) ? v[e] : (_Float16)0.0f;
+                        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n], acc[t], 0, 0, 0);
+                    }
+            }
+        } else {
+            // V: elements ND m .. ND m + ND - 1 of key 32 k + 8 (r / 4) + 4 h + r % 4
+            typedef float vrow __attribute__((ext_vector_type(ND)));
+            auto v_at = [&](int k, int r) {
+                return *reinterpret_cast<const vrow*>(vt + (32 * k + 8 * (r / 4) + 4 * h + r % 4) * ROW + m * ND * 4);
+            };
+            bool special = false;
+            if (!whole) {
+                bool odd = false;
+#pragma unroll 4
+                for (int r = 0; r < TILE; r += 2) {
+                    const vrow v = *reinterpret_cast<const vrow*>(vt + (r + h) * ROW + m * ND * 4);
+#pragma unroll
+                    for (int t = 0; t < ND; ++t) odd |= !finite(v[t]);
+                }
+                special = __any(odd);
+            }
+            if (special)
+                add_nonfinite<DT, DP>(acc, vt, lane, max(w_lo - j, 0), min(min(w_hi, to) - j, TILE), lo - j, hi - j, ok);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    vrow v = v_at(k, r);
+                    if (special) {
+#pragma unroll
+                        for (int t = 0; t < ND; ++t) v[t] = finite(v[t]) ? v[t] : 0.0f;
+                    }
+#pragma unroll
+                    for (int t = 0; t < ND; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[t], sc[k][r], acc[t], 0, 0, 0);
+                }
+        }
+    }
+
+    sum += __shfl_xor(sum, 32, WAVE);
+    if (!row) return;
+    // acc[t][i]: element 32 t + 8 (i / 4) + 4 h + i % 4 (f16), ND (8 (i / 4) + 4 h + i % 4) + t (f32)
+    const int64_t at = (((int64_t)flat * a.c.kv_heads + kvh) * a.splits + sp) * a.rows + my;
+    auto put = [&](int e, f4 o) {
+        if (!FULL && e >= d) return;
+        if (n_split > 1) *reinterpret_cast<f4*>(a.part + at * d + e) = o;
+        else store_row<DT>(a, tok, head, e, o, ref, sum);
+    };
+    if (n_split > 1 && h == 0) a.part_ml[at] = make_float2(ref, sum);
+    if constexpr (DT == F16) {
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                put(32 * t + 8 * (i / 4) + 4 * h, f4{acc[t][i], acc[t][i + 1], acc[t][i + 2], acc[t][i + 3]});
+    } else {
+        float flat_out[16 * ND];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int t = 0; t < ND; ++t) flat_out[i * ND + t] = acc[t][i];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+#pragma unroll
+            for (int x = 0; x < 4 * ND; x += 4)
+                put(ND * (8 * (i / 4) + 4 * h) + x, f4{flat_out[i * ND + x], flat_out[i * ND + x + 1],
+                                                       flat_out[i * ND + x + 2], flat_out[i * ND + x + 3]});
+    }
+}
+
 // Join of a row's splits, in their order: four elements per thread.
 template <int DT>
 __global__ __launch_bounds__(WAVE) void k_attn_join(AttnArgs a) {
-    const int s = blockIdx.z, kvh = blockIdx.y, d = a.c.head_dim, pieces = d / 4;
+    const int flat = blockIdx.z, kvh = blockIdx.y, d = a.c.head_dim, pieces = d / 4;
+    const int n = min(a.part_n[flat], a.splits);
+    if (n <= 1) return;                           // written by the only one
+    int s = flat, r0 = 0;
+    if (a.rows > FEW_ROWS && !tile_at(a, flat, a.rows, a.most_rows, s, r0)) return;
     const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
     const int i = blockIdx.x * WAVE + threadIdx.x, r = i / pieces, e = (i - r * pieces) * 4;
-    if (r >= min((t1 - t0) * a.group, a.rows)) return;
-    const int n = min(a.part_n[s], a.splits);
-    if (n <= 1) return;                           // written by the only one
-    const int64_t at = ((int64_t)s * a.c.kv_heads + kvh) * a.splits * a.rows + r;
+    if (r >= min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)a.rows)) return;
+    const int64_t at = ((int64_t)flat * a.c.kv_heads + kvh) * a.splits * a.rows + r;
     float top = -INFINITY, l = 0.0f;
 #pragma unroll 8
     for (int k = 0; k < n; ++k) top = fmaxf(top, a.part_ml[at + (int64_t)k * a.rows].x);
@@ -494,7 +939,7 @@ __global__ __launch_bounds__(WAVE) void k_attn_join(AttnArgs a) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[c] += f == 0.0f ? 0.0f : f * v[c];
     }
-    store_row<DT>(a, t0 + r / a.group, kvh * a.group + r % a.group, e, o, top, l);
+    store_row<DT>(a, t0 + (r0 + r) / a.group, kvh * a.group + (r0 + r) % a.group, e, o, top, l);
 }
 
 }  // namespace pi

@@ -12,101 +12,54 @@ using namespace pi;
 
 namespace {
 
-constexpr int MAXD_PER_LANE = PI_MAX_HEAD_DIM / WAVE;
-
-// One wave per row and query head: a lane scores one key of 64, then owns every
-// 64th element of the output.
-template <int DT>
-__global__ __launch_bounds__(WAVE) void k_attn(AttnArgs a) {
-    typedef typename ElemT<DT>::T T;
-    __shared__ float q[PI_MAX_HEAD_DIM], ps[WAVE];
-    __shared__ int64_t at[WAVE];
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-    const int s = seq_of_row(a.b, t);
-    if (s >= a.b.n_seqs || a.b.q_start[s] > t) return;
-    const int d = a.c.head_dim, kvh = h / a.group;
-    const int len = clamped_len(a.b, a.c.page_shift, s);
-    const int pos = len - (a.b.q_start[s + 1] - t);
-    int lo = a.first ? max(a.first[t], 0) : 0, hi = pos + 1;
-    if (a.window > 0 && pos - a.window + 1 > lo) lo = pos - a.window + 1;
-    if (a.prefix) hi = max(hi, a.prefix[s]);
-    hi = min(hi, len);
-    const T* qr = (const T*)a.q + t * a.q_ts + h * a.q_hs;
-    for (int e = lane; e < d; e += WAVE) q[e] = (float)qr[e] * a.scale;
-    __syncthreads();
-    const float slope = a.slopes ? a.slopes[h] : 0.0f;
-    float m = -INFINITY, l = 0.0f, acc[MAXD_PER_LANE] = {};
-    for (int j0 = lo; j0 < hi; j0 += WAVE) {
-        const int j = j0 + lane;
-        float x = -INFINITY;
-        at[lane] = -1;
-        if (j < hi) {
-            const int page = a.b.table[(int64_t)s * a.b.table_stride + (j >> a.c.page_shift)];
-            if (page >= 0 && page < a.c.pages) {
-                const int64_t row = ((int64_t)page * a.c.kv_heads + kvh) * a.c.page_size + (j & (a.c.page_size - 1));
-                at[lane] = row;
-                const T* k = (const T*)a.c.k + row * d;
-                x = 0.0f;
-                for (int e = 0; e < d; ++e) x = fmaf(q[e], (float)k[e], x);
-                if (a.cap > 0.0f) x = a.cap * tanhf(x / a.cap);
-                x -= slope * (float)abs(pos - j);
-            }
-        }
-        float mx = x;
-        for (int o = WAVE / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, WAVE));
-        mx = fmaxf(mx, m);
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        const float p = at[lane] >= 0 ? expf(x - ref) : 0.0f;
-        const float alpha = expf(m - ref);
-        m = mx;
-        l = l * alpha + wave_sum(p);
-        ps[lane] = p;
-        __syncthreads();
-        for (int e = 0; e < MAXD_PER_LANE; ++e) acc[e] *= alpha;
-        for (int i = 0; i < min(WAVE, hi - j0); ++i) {
-            if (at[i] < 0) continue;
-            const T* v = (const T*)a.c.v + at[i] * d;
-            for (int e = 0; e < MAXD_PER_LANE; ++e)
-                if (lane + e * WAVE < d) acc[e] = fmaf(ps[i], (float)v[lane + e * WAVE], acc[e]);
-        }
-        __syncthreads();
-    }
-    T* o = (T*)a.out + t * a.o_ts + h * a.o_hs;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int e = 0; e < MAXD_PER_LANE; ++e)
-        if (lane + e * WAVE < d) o[lane + e * WAVE] = (T)(acc[e] * inv);
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.q_heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
-}
-
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Which kernel a call runs, how the keys are split, and the workspace for it.
 struct Plan {
     bool few;                  // at most 16 rows per sequence and key head
+    int64_t tiles, most_rows;
     int rows, chunk, splits;
     size_t part, ml, n, bytes; // offsets in the workspace, its size
 };
 
+// Keys per split so that about `want` workgroups have work when every sequence is max_len long;
+// none smaller than `least` keys (the join costs as much as reading some hundred keys).
+void split_keys(Plan& p, int64_t alone, int64_t want, int64_t least, int max_len) {
+    const int64_t n = std::max<int64_t>(1, want / std::max<int64_t>(1, alone));
+    const int64_t chunk = std::max<int64_t>(least, ((int64_t)max_len + n - 1) / n);
+    p.chunk = (int)std::min<int64_t>((chunk + 127) / 128 * 128, 1 << 30);
+    p.splits = std::max(1, (int)(((int64_t)max_len + p.chunk - 1) / p.chunk));
+}
+
 Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
     Plan p{};
-    const int64_t rows = (int64_t)std::min(b->max_new, b->n_tokens) * (q_heads / c->kv_heads);
-    p.few = rows <= FEW_ROWS;
-    p.rows = (int)std::min<int64_t>(rows, FEW_ROWS);
-    p.splits = 1;
-    p.chunk = 1 << 30;
+    const int group = q_heads / c->kv_heads;
+    p.most_rows = (int64_t)std::min(b->max_new, b->n_tokens) * group;
+    p.few = p.most_rows <= FEW_ROWS;
     if (p.few) {
-        const int64_t alone = std::max<int64_t>(1, (int64_t)b->n_seqs * c->kv_heads);
-        const int64_t want = std::max<int64_t>(1, 2048 / alone);
-        const int64_t chunk = std::max<int64_t>(256, ((int64_t)b->max_len + want - 1) / want);
-        p.chunk = (int)std::min<int64_t>((chunk + 127) / 128 * 128, 1 << 30);
-        p.splits = std::max(1, (int)(((int64_t)b->max_len + p.chunk - 1) / p.chunk));
+        p.tiles = b->n_seqs;
+        p.rows = (int)p.most_rows;
+        split_keys(p, p.tiles * c->kv_heads, 2048, 256, b->max_len);
+    } else {
+        p.tiles = std::min((int64_t)b->n_tokens * group / MANY_ROWS + b->n_seqs,
+                           b->n_seqs * ((p.most_rows + MANY_ROWS - 1) / MANY_ROWS));
+        p.rows = MANY_ROWS;
+        split_keys(p, p.tiles * c->kv_heads, 512, 512, b->max_len);
     }
     p.part = 0;
-    const size_t slots = p.splits > 1 ? (size_t)b->n_seqs * c->kv_heads * p.splits * p.rows : 0;
+    const size_t slots = p.splits > 1 ? (size_t)p.tiles * c->kv_heads * p.splits * p.rows : 0;
     p.ml = align256(slots * c->head_dim * 4);
     p.n = p.ml + align256(slots * 8);
-    p.bytes = p.n + align256(std::max<size_t>((size_t)b->n_seqs * 4, 4));
+    p.bytes = p.n + align256(std::max<size_t>((size_t)p.tiles * 4, 4));
     return p;
+}
+
+template <int DT>
+pi_status launch_join(const AttnArgs& a, hipStream_t s) {
+    if (a.splits == 1) return PI_OK;
+    const int pieces = a.rows * (a.c.head_dim / 4);
+    return launch(PI_K_ATTN_JOIN, k_attn_join<DT>, dim3((pieces + WAVE - 1) / WAVE, a.c.kv_heads, a.tiles), dim3(WAVE),
+                  0, s, a);
 }
 
 template <int DT, int DP, bool FULL>
@@ -114,24 +67,36 @@ pi_status launch_few(const AttnArgs& a, hipStream_t s) {
     auto kern = k_attn_few<DT, DP, FULL>;
     TRY(allow_lds(kern, few_lds<DP>()));
     TRY(launch(PI_K_ATTN, kern, dim3(a.splits, a.c.kv_heads, a.b.n_seqs), dim3(WAVE * FEW_WAVES), few_lds<DP>(), s, a));
-    if (a.splits == 1) return PI_OK;
-    const int pieces = a.rows * (a.c.head_dim / 4);
-    return launch(PI_K_ATTN_JOIN, k_attn_join<DT>, dim3((pieces + WAVE - 1) / WAVE, a.c.kv_heads, a.b.n_seqs), dim3(WAVE),
-                  0, s, a);
+    return launch_join<DT>(a, s);
+}
+
+template <int DT, int DP, bool FULL, bool RULES>
+pi_status launch_many(const AttnArgs& a, hipStream_t s) {
+    auto kern = k_attn_many<DT, DP, FULL, RULES>;
+    TRY(allow_lds(kern, many_lds<DT, DP>()));
+    const int64_t items = (int64_t)a.tiles * a.c.kv_heads * a.splits;
+    CHECK(items <= 1 << 23, PI_ERR_SHAPE, "too many rows for one call (%lld tiles of %d)", (long long)items, MANY_ROWS);
+    const int grid = (int)((items + XCDS - 1) / XCDS * XCDS);
+    TRY(launch(PI_K_ATTN, kern, dim3(grid), dim3(WAVE * MANY_WAVES), many_lds<DT, DP>(), s, a));
+    return launch_join<DT>(a, s);
+}
+
+template <int DT, int DP, bool FULL>
+pi_status attend(const AttnArgs& a, const Plan& p, hipStream_t s) {
+    if (p.few) return launch_few<DT, DP, FULL>(a, s);
+    if (a.cap > 0.0f || a.slopes || a.scale == 0.0f) return launch_many<DT, DP, FULL, true>(a, s);
+    return launch_many<DT, DP, FULL, false>(a, s);
 }
 
 template <int DT>
-pi_status attend(const AttnArgs& a, const Plan& p, int q_heads, hipStream_t s) {
+pi_status attend_dim(const AttnArgs& a, const Plan& p, hipStream_t s) {
     const int d = a.c.head_dim;
-    if (p.few) {
-        if (d == 64) return launch_few<DT, 64, true>(a, s);
-        if (d < 64) return launch_few<DT, 64, false>(a, s);
-        if (d == 128) return launch_few<DT, 128, true>(a, s);
-        if (d < 128) return launch_few<DT, 128, false>(a, s);
-        if (d == 256) return launch_few<DT, 256, true>(a, s);
-        return launch_few<DT, 256, false>(a, s);
-    }
-    return launch(PI_K_ATTN, k_attn<DT>, dim3(a.b.n_tokens, q_heads), dim3(WAVE), 0, s, a);
+    if (d == 64) return attend<DT, 64, true>(a, p, s);
+    if (d < 64) return attend<DT, 64, false>(a, p, s);
+    if (d == 128) return attend<DT, 128, true>(a, p, s);
+    if (d < 128) return attend<DT, 128, false>(a, p, s);
+    if (d == 256) return attend<DT, 256, true>(a, p, s);
+    return attend<DT, 256, false>(a, p, s);
 }
 
 pi_status check_q_heads(const pi_kv_cache* c, int q_heads) {
@@ -186,14 +151,16 @@ pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_s
     a.slopes = rule->slopes;
     a.prefix = rule->prefix;
     a.first = rule->first;
+    a.tiles = (int)p.tiles;
     a.rows = p.rows;
+    a.most_rows = p.most_rows;
     a.chunk = p.chunk;
     a.splits = p.splits;
     a.part = (float*)((uint8_t*)ws + p.part);
     a.part_ml = (float2*)((uint8_t*)ws + p.ml);
     a.part_n = (int*)((uint8_t*)ws + p.n);
     hipStream_t s = (hipStream_t)stream;
-    return cache->dtype == PI_F32 ? attend<F32>(a, p, q_heads, s) : attend<F16>(a, p, q_heads, s);
+    return cache->dtype == PI_F32 ? attend_dim<F32>(a, p, s) : attend_dim<F16>(a, p, s);
 }
 
 }  // extern "C"

@@ -69,7 +69,7 @@ inline pi_status check_layer(const pi_kv_cache* c, int layer) {
 
 inline pi_status check_batch(const pi_seq_batch* b) {
     CHECK(b, PI_ERR_ARG, "NULL batch");
-    CHECK(b->n_seqs >= 0 && b->n_seqs <= (1 << 20), PI_ERR_SHAPE, "batch: n_seqs must be in 0..2^20");
+    CHECK(b->n_seqs >= 0 && b->n_seqs <= 65535, PI_ERR_SHAPE, "batch: n_seqs must be in 0..65535");
     CHECK(b->n_tokens >= 0 && b->n_tokens <= (1 << 23), PI_ERR_SHAPE, "batch: n_tokens must be in 0..2^23");
     CHECK(b->max_new >= 0 && b->max_len >= 0, PI_ERR_SHAPE, "batch: max_new and max_len must be >= 0");
     if (b->n_seqs == 0 || b->n_tokens == 0) return PI_OK;
