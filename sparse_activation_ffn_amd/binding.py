@@ -187,19 +187,24 @@ def ptr(t) -> Optional[int]:
 def stream_handle(stream=None) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
+_dtypes: dict = {}
+
+
 def dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return PI_F32
-    if t.dtype == torch.float16:
-        return PI_F16
-    raise TypeError(f"no pi dtype for {t.dtype}")
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        import torch
+        _dtypes.update({torch.float32: PI_F32, torch.float16: PI_F16})
+        code = _dtypes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"no pi dtype for {t.dtype}")
+    return code
 
 
 # ---- the C entry points, same names -----------------------------------------
@@ -372,12 +377,12 @@ def pi_rope_append(cache: KvCache, layer: int, batch: SeqBatch, rope: Rope, q, q
     """q, q_out [tokens][q_heads][head_dim] (both None: keys and values only), k and v
     [tokens][kv_heads][head_dim]; the elements of a head contiguous, other strides free."""
     hq = 0 if q is None else q.shape[1]
+    hk, dt, d, n = cache.kv_heads, cache.dtype, cache.head_dim, batch.n_tokens
     _check(lib().pi_rope_append(
         C.byref(cache), layer, C.byref(batch), C.byref(rope), ptr(positions), hq,
-        None if q is None else C.byref(_rows(q, cache, batch, hq)),
-        None if q_out is None else C.byref(_rows(q_out, cache, batch, hq)),
-        C.byref(_rows(k, cache, batch, cache.kv_heads)),
-        C.byref(_rows(v, cache, batch, cache.kv_heads)), stream_handle(stream)))
+        None if q is None else _rows(q, dt, d, n, hq),
+        None if q_out is None else _rows(q_out, dt, d, n, hq),
+        _rows(k, dt, d, n, hk), _rows(v, dt, d, n, hk), stream_handle(stream)))
 
 
 def pi_attention_workspace_bytes(cache: KvCache, batch: SeqBatch, q_heads: int) -> int:
@@ -387,11 +392,11 @@ def pi_attention_workspace_bytes(cache: KvCache, batch: SeqBatch, q_heads: int) 
 def pi_paged_attention(cache: KvCache, layer: int, batch: SeqBatch, rule: ScoreRule, q, out,
                        lse=None, ws=None, stream=None):
     """q and out [tokens][q_heads][head_dim], lse [tokens][q_heads] float32 or None."""
-    hq = q.shape[1]
+    hq, dt, d, n = q.shape[1], cache.dtype, cache.head_dim, batch.n_tokens
     _check(lib().pi_paged_attention(
-        C.byref(cache), layer, C.byref(batch), C.byref(rule), hq,
-        C.byref(_rows(q, cache, batch, hq)), C.byref(_rows(out, cache, batch, hq)), ptr(lse),
-        ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
+        C.byref(cache), layer, C.byref(batch), C.byref(rule), hq, _rows(q, dt, d, n, hq),
+        _rows(out, dt, d, n, hq), ptr(lse), ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
 
 
 def pi_pages_workspace_bytes(state: PageState, n: int) -> int:
@@ -520,15 +525,17 @@ def _int32(name: str, t, shape):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
 
 
-def _rows(t, cache: KvCache, batch: SeqBatch, heads: int) -> Rows:
-    """[tokens][heads][head_dim] as the library sees it; the shape is checked here, where it is known."""
-    if t.dim() != 3 or t.shape[0] < batch.n_tokens or t.shape[1] != heads or \
-            t.shape[2] != cache.head_dim or t.stride(2) != 1:
-        raise ValueError(f"need [{batch.n_tokens}][{heads}][{cache.head_dim}] with contiguous heads, "
-                         f"got {tuple(t.shape)} with strides {t.stride()}")
-    if dtype_code(t) != cache.dtype:
+def _rows(t, dtype: int, head_dim: int, n_tokens: int, heads: int):
+    """Reference to [tokens][heads][head_dim] as the library sees it; checked here, where the
+    shape is known."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != heads or shape[2] != head_dim or \
+            strides[2] != 1:
+        raise ValueError(f"need [{n_tokens}][{heads}][{head_dim}] with contiguous heads, "
+                         f"got {tuple(shape)} with strides {strides}")
+    if dtype_code(t) != dtype:
         raise TypeError("q, k, v and the output have the cache's dtype")
-    return Rows(ptr(t), t.stride(0), t.stride(1))
+    return C.byref(Rows(t.data_ptr(), strides[0], strides[1]))
 
 
 def row_slice(t, lo: int, hi: int):

@@ -561,20 +561,33 @@ __device__ __forceinline__ bool tile_at(const AttnArgs& a, int flat, int tile, i
 
 __device__ __forceinline__ bool finite(float f) { return f - f == 0.0f; }
 
-// output element of acc[t][i] in lane half h
-template <int DT, int DP>
-__device__ __forceinline__ int out_elem(int t, int i, int h) {
-    const int r = 8 * (i / 4) + 4 * h + i % 4;
-    return DT == F16 ? 32 * t + r : DP / 32 * r + t;
+template <int DT>
+__device__ __forceinline__ bool nonfinite(u4 w) {
+    if (DT == F16) return (nonfinite_h2(w.x) | nonfinite_h2(w.y) | nonfinite_h2(w.z) | nonfinite_h2(w.w)) != 0;
+    return !(finite(bits_f(w.x)) && finite(bits_f(w.y)) && finite(bits_f(w.z)) && finite(bits_f(w.w)));
 }
 
-// Where some row of the wave does not see every key of a tile, an infinity or NaN in V would reach it through
-// 0 * V.  Such elements are left out of the product, and added here to the rows that see them: of keys
-// k0 <= k < k1 of the tile with a page (ok), each lane's row sees lo <= k < hi.
+// infinities and NaN replaced by 0
+template <int DT>
+__device__ __forceinline__ u4 only_finite(u4 w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (DT == F16) {
+            const unsigned odd = nonfinite_h2(w[i]);
+            w[i] &= ~((odd >> 15) * 0xffffu);      // both carries: 0x80000000 and 0x8000
+        } else {
+            w[i] = finite(bits_f(w[i])) ? w[i] : 0u;
+        }
+    }
+    return w;
+}
+
+// The infinities and NaN in V of keys k0 <= k < k1 of a tile with a page (ok), added to the rows that see them:
+// each lane's row sees lo <= k < hi.
 template <int DT, int DP>
 __device__ __forceinline__ void add_nonfinite(f16v* acc, const uint8_t* vt, int lane, int k0, int k1, int lo, int hi,
                                               uint64_t ok) {
-    constexpr int ES = Many<DT, DP>::ES, ROW = Many<DT, DP>::ROW, ND = DP / 32, EV = 16 / ES;
+    constexpr int ROW = Many<DT, DP>::ROW, ND = DP / 32;
     for (int k = k0; k < k1; ++k) {
         if (!((ok >> k) & 1)) continue;
         bool odd = false;
@@ -584,14 +597,23 @@ __device__ __forceinline__ void add_nonfinite(f16v* acc, const uint8_t* vt, int 
         }
         if (!__any(odd)) continue;
         const bool sees = k >= lo && k < hi;
+        const int h = lane / 32;
 #pragma unroll
         for (int t = 0; t < ND; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = out_elem<DT, DP>(t, i, lane / 32);
-                const uint8_t* p = vt + k * ROW + v_piece<DT, ROW>(k, e / EV) * 16 + (e % EV) * ES;
-                const float f = DT == F16 ? half_f(*reinterpret_cast<const uint16_t*>(p)) : *reinterpret_cast<const float*>(p);
-                acc[t][i] += sees && !finite(f) ? f : 0.0f;
+            for (int i = 0; i < 16; i += 4) {      // acc[t][i .. i + 3]: see the end of k_attn_many
+                float f[4];
+                if constexpr (DT == F16) {
+                    const int piece = v_piece<DT, ROW>(k, 4 * t + i / 4);
+                    const u2 w = *reinterpret_cast<const u2*>(vt + k * ROW + piece * 16 + 8 * h);
+                    f[0] = half_lo(w.x), f[1] = half_hi(w.x), f[2] = half_lo(w.y), f[3] = half_hi(w.y);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        f[c] = reinterpret_cast<const float*>(vt + k * ROW)[ND * (2 * i + 4 * h + c) + t];
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[t][i + c] += sees && !finite(f[c]) ? f[c] : 0.0f;
             }
     }
 }
@@ -654,14 +676,20 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     if (lane == 0) {
         scratch[wave] = w_lo;
         scratch[MANY_WAVES + wave] = w_hi;
+        scratch[2 * MANY_WAVES + wave] = in_lo;
+        scratch[3 * MANY_WAVES + wave] = in_hi;
     }
     __syncthreads();
-    int start = 0x7fffffff, end = 0;
+    int start = 0x7fffffff, end = 0, all_lo = 0, all_hi = 0x7fffffff;
 #pragma unroll
     for (int w = 0; w < MANY_WAVES; ++w) {
         start = min(start, scratch[w]);
         end = max(end, scratch[MANY_WAVES + w]);
+        all_lo = max(all_lo, scratch[2 * MANY_WAVES + w]);
+        all_hi = min(all_hi, scratch[3 * MANY_WAVES + w]);
     }
+    all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
     __syncthreads();
     start = __builtin_amdgcn_readfirstlane(end > 0 ? start & ~(TILE - 1) : 0);
     end = __builtin_amdgcn_readfirstlane(end);
@@ -697,9 +725,8 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
         __syncthreads();
     }
     auto page_of = [&](int j) { return table[min((j + lane) >> shift, last_page)]; };
-    // keys j .. j + TILE - 1 into buffer b; `page` holds the page of key j + lane
-    auto load_tile = [&](int j, int page, int b) {
-        uint8_t* kt = smem + b * 2 * M::BYTES;
+    // keys j .. j + TILE - 1 into a buffer; `page` holds the page of key j + lane
+    auto load_tile = [&](int j, int page, uint8_t* __restrict__ kt) {
         const int safe = (unsigned)page < (unsigned)a.c.pages ? page : 0;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -717,25 +744,45 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     for (int t = 0; t < ND; ++t) acc[t] = f16v{};
     float ref = -INFINITY, sum = 0.0f;
 
+    // byte offsets of this lane's reads in a buffer, before c and t are put in
+    const int k_base = m * ROW + k_piece<ROW>(m, h) * 16;
+    const int v_row = 4 * h + lane % 16 / 4, v_elem = 16 * (lane / 16 % 2) + 4 * (lane % 4);
+    const int v_base = v_row * ROW + v_piece<DT, ROW>(v_row, v_elem / 8) * 16 + v_elem % 8 * 2;
+
     int page = 0, page_next = 0;
     if (from < to) {
         page = page_of(from);
-        load_tile(from, page, 0);
+        load_tile(from, page, smem);
         page_next = page_of(from + TILE);
     }
-    int b = 0;
-    for (int j = from; j < to; j += TILE, b ^= 1) {
+    // one tile: its keys and values lie at cur, the next tile's go to next
+    auto step = [&](int j, uint8_t* __restrict__ cur, uint8_t* __restrict__ next) {
         wait_loads();
         __syncthreads();                           // tile j is there, and every wave is done with the other buffer
         const uint64_t ok = __ballot((unsigned)page < (unsigned)a.c.pages);
         if (j + TILE < to) {
-            load_tile(j + TILE, page_next, b ^ 1);
+            load_tile(j + TILE, page_next, next);
             page = page_next;
             page_next = page_of(j + 2 * TILE);
         }
-        if (j >= w_hi || j + TILE <= w_lo) continue;   // no row of this wave sees these keys
-        const uint8_t* kt = smem + b * 2 * M::BYTES;
-        const uint8_t* vt = kt + M::BYTES;
+        constexpr uint64_t ALL = TILE == 64 ? ~0ull : (1ull << (TILE % 64)) - 1;
+        const bool pages = (ok & ALL) == ALL, idle = j >= w_hi || j + TILE <= w_lo;
+        if (!(j >= all_lo && j + TILE <= all_hi && j + TILE <= to && pages)) {
+            // Where some row does not see every key, an infinity or NaN in V would reach it through 0 * V: such
+            // elements go to the rows that see them one by one, and become 0 for the product.
+            u4* vt = reinterpret_cast<u4*>(cur + M::BYTES);
+            bool odd = false;
+            for (int i = threadIdx.x; i < M::BYTES / 16; i += WAVE * MANY_WAVES) odd |= nonfinite<DT>(vt[i]);
+            if (__syncthreads_or(odd)) {
+                if (!idle)
+                    add_nonfinite<DT, DP>(acc, cur + M::BYTES, lane, max(w_lo - j, 0), min(min(w_hi, to) - j, TILE), lo - j,
+                                          hi - j, ok);
+                __syncthreads();
+                for (int i = threadIdx.x; i < M::BYTES / 16; i += WAVE * MANY_WAVES) vt[i] = only_finite<DT>(vt[i]);
+                __syncthreads();
+            }
+        }
+        if (idle) return;                          // no row of this wave sees these keys
 
         f16v sc[KB];
 #pragma unroll
@@ -743,7 +790,8 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
             sc[k] = f16v{};
 #pragma unroll
             for (int c = 0; c < NK; ++c) {
-                const u4 kk = *reinterpret_cast<const u4*>(kt + (k * 32 + m) * ROW + k_piece<ROW>(k * 32 + m, 2 * c + h) * 16);
+                // piece 2c + h of row 32 k + m: the permutation leaves an exclusive or with 2c
+                const u4 kk = *reinterpret_cast<const u4*>(cur + ((k_base ^ (c * 32)) + k * 32 * ROW));
                 if constexpr (DT == F16) {
                     sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kk), __builtin_bit_cast(h8, q[c]),
                                                                    sc[k], 0, 0, 0);
@@ -755,28 +803,43 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
             }
         }
         // key of score r of block k: j + 32 k + 8 (r / 4) + 4 h + r % 4
-        constexpr uint64_t ALL = TILE == 64 ? ~0ull : (1ull << (TILE % 64)) - 1;
-        const bool whole = j >= in_lo && j + TILE <= in_hi && j + TILE <= to && (ok & ALL) == ALL;
+        const bool whole = j >= in_lo && j + TILE <= in_hi && j + TILE <= to && pages;
         if (RULES) {
 #pragma unroll
-            for (int k = 0; k < KB; ++k)
+            for (int k = 0; k < KB; ++k) sc[k] *= scale;
+            if (a.cap > 0.0f) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float v = sc[k][r] * scale;
-                    if (a.cap > 0.0f) v = a.cap * LOG2E * tanh_of<DT>(v);
-                    if (a.slopes) v -= slope * (float)abs(pos - (j + 32 * k + 8 * (r / 4) + 4 * h + r % 4));
-                    sc[k][r] = v;
-                }
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[k][r] = a.cap * LOG2E * tanh_of<DT>(sc[k][r]);
+            }
+            if (a.slopes) {
+                const float away = (float)(pos - j - 4 * h);
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r]);
+            }
         }
-        auto sees = [&](int k, int r) {
-            const int key = 32 * k + 8 * (r / 4) + 4 * h + r % 4;
-            return j + key >= lo && j + key < hi && j + key < to && ((ok >> key) & 1);
-        };
         if (!whole) {
+            // seen: lo <= key < min(hi, to), as one unsigned comparison relative to this lane's first key
+            const int at = lo - j - 4 * h;
+            const unsigned many = max(min(hi, to) - lo, 0);
 #pragma unroll
             for (int k = 0; k < KB; ++k)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) sc[k][r] = sees(k, r) ? sc[k][r] : -INFINITY;
+                for (int r = 0; r < 16; ++r)
+                    sc[k][r] = (unsigned)(32 * k + 8 * (r / 4) + r % 4 - at) < many ? sc[k][r] : -INFINITY;
+            if (!pages) {                          // a page that is none hides its 8 keys or more
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sc[k][r + i] = (ok >> (32 * k + 2 * r)) & 1 ? sc[k][r + i] : -INFINITY;
+            }
         }
         float top = sc[0][0];
 #pragma unroll
@@ -787,7 +850,8 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
         top *= unit;
         if (__any(top > ref + SLACK)) {
             top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-            const float now = fmaxf(ref, top), f = weight_of(ref, now);
+            // (nothing is summed while ref is -inf but infinities, which no factor may turn into NaN)
+            const float now = fmaxf(ref, top), f = ref == -INFINITY ? 1.0f : fmaxf(weight_of(ref, now), 1e-37f);
             ref = now;
             sum *= f;
 #pragma unroll
@@ -810,77 +874,38 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
             for (int n = 0; n < 2 * KB; ++n)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) p[n][e] = (_Float16)sc[n / 2][8 * (n % 2) + e];
-            // V^T: elements 32 t + m of these keys
+            // V^T: elements 32 t + m of these keys (rows 16 n + 4 h .. + 3, then 8 further on, where the
+            // permutation is the same)
             auto v_at = [&](int t, int n) {
-                const int l = lane % 16, r = 16 * n + 4 * h + l / 4, e = 32 * t + 16 * ((lane / 16) % 2) + 4 * (l % 4);
-                const uint8_t* p0 = vt + r * ROW + v_piece<DT, ROW>(r, e / 8) * 16 + (e % 8) * 2;
+                const uint8_t* p0 = cur + ((v_base ^ (t * 64)) + M::BYTES + n * 16 * ROW);
                 const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p0);
-                // rows 8 further on: the permutation repeats
                 const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(p0 + 8 * ROW));
                 return __builtin_bit_cast(h8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
             };
-            bool special = false;
-            if (!whole) {
-                unsigned odd = 0;
-#pragma unroll 1
-                for (int t = 0; t < ND; ++t)
 #pragma unroll
-                    for (int n = 0; n < 2 * KB; ++n) {
-                        const u4 w = __builtin_bit_cast(u4, v_at(t, n));
-                        odd |= nonfinite_h2(w.x) | nonfinite_h2(w.y) | nonfinite_h2(w.z) | nonfinite_h2(w.w);
-                    }
-                special = __any(odd != 0);
-            }
-            if (!special) {
+            for (int t = 0; t < ND; ++t)
 #pragma unroll
-                for (int t = 0; t < ND; ++t)
-#pragma unroll
-                    for (int n = 0; n < 2 * KB; ++n)
-                        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_at(t, n), p[n], acc[t], 0, 0, 0);
-            } else {
-                add_nonfinite<DT, DP>(acc, vt, lane, max(w_lo - j, 0), min(min(w_hi, to) - j, TILE), lo - j, hi - j, ok);
-#pragma unroll
-                for (int t = 0; t < ND; ++t)
-#pragma unroll
-                    for (int n = 0; n < 2 * KB; ++n) {
-                        h8 v = v_at(t, n);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = finite((float)v[e]) ? v[e] : (_Float16)0.0f;
-                        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n], acc[t], 0, 0, 0);
-                    }
-            }
+                for (int n = 0; n < 2 * KB; ++n)
+                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_at(t, n), p[n], acc[t], 0, 0, 0);
         } else {
             // V: elements ND m .. ND m + ND - 1 of key 32 k + 8 (r / 4) + 4 h + r % 4
             typedef float vrow __attribute__((ext_vector_type(ND)));
             auto v_at = [&](int k, int r) {
-                return *reinterpret_cast<const vrow*>(vt + (32 * k + 8 * (r / 4) + 4 * h + r % 4) * ROW + m * ND * 4);
+                return *reinterpret_cast<const vrow*>(cur + M::BYTES + (32 * k + 8 * (r / 4) + 4 * h + r % 4) * ROW + m * ND * 4);
             };
-            bool special = false;
-            if (!whole) {
-                bool odd = false;
-#pragma unroll 4
-                for (int r = 0; r < TILE; r += 2) {
-                    const vrow v = *reinterpret_cast<const vrow*>(vt + (r + h) * ROW + m * ND * 4);
-#pragma unroll
-                    for (int t = 0; t < ND; ++t) odd |= !finite(v[t]);
-                }
-                special = __any(odd);
-            }
-            if (special)
-                add_nonfinite<DT, DP>(acc, vt, lane, max(w_lo - j, 0), min(min(w_hi, to) - j, TILE), lo - j, hi - j, ok);
 #pragma unroll
             for (int k = 0; k < KB; ++k)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    vrow v = v_at(k, r);
-                    if (special) {
-#pragma unroll
-                        for (int t = 0; t < ND; ++t) v[t] = finite(v[t]) ? v[t] : 0.0f;
-                    }
+                    const vrow v = v_at(k, r);
 #pragma unroll
                     for (int t = 0; t < ND; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[t], sc[k][r], acc[t], 0, 0, 0);
                 }
         }
+    };
+    for (int j = from; j < to; j += 2 * TILE) {
+        step(j, smem, smem + 2 * M::BYTES);
+        if (j + TILE < to) step(j + TILE, smem + 2 * M::BYTES, smem);
     }
 
     sum += __shfl_xor(sum, 32, WAVE);
