@@ -17,6 +17,9 @@
 
 namespace pi {
 
+// on a lambda: part of the kernel, whatever its size
+#define INLINE __attribute__((always_inline))
+
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
@@ -512,7 +515,7 @@ template <int DT, int DP> struct Many {
     static constexpr int BYTES = TILE * ROW;
 };
 
-template <int DT, int DP> constexpr size_t many_lds() { return 4 * Many<DT, DP>::BYTES; }   // K, V, twice
+template <int DT, int DP> constexpr size_t many_lds() { return 4 * Many<DT, DP>::BYTES; }   // K and V, two buffers each
 
 // piece c of row r of a K tile: 16 rows in a row at the same c read 16 different pieces of 256 bytes
 template <int ROW>
@@ -530,6 +533,13 @@ __device__ __forceinline__ int v_piece(int r, int c) {
 __device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// an address that is the same in all lanes, in scalar registers
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = (unsigned)__builtin_amdgcn_readfirstlane((int)v), hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return reinterpret_cast<const uint8_t*>(hi << 32 | lo);
 }
 
 // all loads of this wave have arrived (vmcnt 0, the other counters as they are)
@@ -724,18 +734,33 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
             reinterpret_cast<u4*>(smem)[i] = u4{0, 0, 0, 0};
         __syncthreads();
     }
-    auto page_of = [&](int j) { return table[min((j + lane) >> shift, last_page)]; };
-    // keys j .. j + TILE - 1 into a buffer; `page` holds the page of key j + lane
-    auto load_tile = [&](int j, int page, uint8_t* __restrict__ kt) {
-        const int safe = (unsigned)page < (unsigned)a.c.pages ? page : 0;
+    auto page_of = [&](int j) INLINE { return table[min((j + lane) >> shift, last_page)]; };
+    // what a lane loads of a row: the piece that belongs where its 16 bytes go in LDS
+    unsigned k_off[LOADS], v_off[LOADS];
+    bool k_ok[LOADS], v_ok[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int r = lane / NC, row_in_tile = (wave * LOADS + i) * RPI + r;
+        const int kc = k_piece<ROW>(row_in_tile, lane % NC), vc = v_piece<DT, ROW>(row_in_tile, lane % NC);
+        k_off[i] = r * d * ES + kc * 16;
+        v_off[i] = r * d * ES + vc * 16;
+        k_ok[i] = kc * EV < d;
+        v_ok[i] = vc * EV < d;
+    }
+    // Keys j .. j + TILE - 1 of K or V into a buffer; `page` holds the page of key j + lane.  The rows of one
+    // instruction lie in one page, one after the other: a scalar address and fixed lane offsets.
+    static_assert(RPI <= 8, "a page holds 8 rows or more");
+    auto load_tile = [&](const uint8_t* base, int j, int page, const unsigned (&off)[LOADS], const bool (&has)[LOADS],
+                         uint8_t* __restrict__ to_lds) INLINE {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int first = (wave * LOADS + i) * RPI, r = first + lane / NC, at = lane % NC;
-            const int p = __shfl(safe, r, WAVE);
-            const int64_t off = p * page_bytes + (int64_t)(head_off + ((j + r) & (ps - 1))) * d * ES;
-            const int kc = k_piece<ROW>(r, at), vc = v_piece<DT, ROW>(r, at);
-            if (FULL || kc * EV < d) load_to_lds(a.c.k + off + kc * 16, kt + first * ROW);
-            if (FULL || vc * EV < d) load_to_lds(a.c.v + off + vc * 16, kt + M::BYTES + first * ROW);
+            const int first = (wave * LOADS + i) * RPI;
+            const int id = __builtin_amdgcn_readlane(page, first);
+            const int p = (unsigned)id < (unsigned)a.c.pages ? id : 0;
+            const uint8_t* at = scalar(base + (p * page_bytes + (int64_t)(head_off + ((j + first) & (ps - 1))) * d * ES));
+            unsigned lane_off = off[i];
+            asm volatile("" : "+v"(lane_off));     // (else it is kept as 64 bits, and the address is formed in vector registers)
+            if (FULL || has[i]) load_to_lds(at + lane_off, to_lds + first * ROW);
         }
     };
 
@@ -749,19 +774,56 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     const int v_row = 4 * h + lane % 16 / 4, v_elem = 16 * (lane / 16 % 2) + 4 * (lane % 4);
     const int v_base = v_row * ROW + v_piece<DT, ROW>(v_row, v_elem / 8) * 16 + v_elem % 8 * 2;
 
+    const float unit = RULES ? 1.0f : scale;
     int page = 0, page_next = 0;
-    if (from < to) {
-        page = page_of(from);
-        load_tile(from, page, smem);
-        page_next = page_of(from + TILE);
-    }
+
+    // cap and bias of the scores of tile j; score r of block k belongs to key j + 32 k + 8 (r / 4) + 4 h + r % 4
+    auto by_rule = [&](f16v (&sc)[KB], int j) INLINE {
+        if (RULES) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k) sc[k] *= scale;
+            if (a.cap > 0.0f) {
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[k][r] = a.cap * LOG2E * tanh_of<DT>(sc[k][r]);
+            }
+            if (a.slopes) {
+                const float away = (float)(pos - j - 4 * h);
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r]);
+            }
+        }
+    };
+    // moves the reference when a score passes it by too much
+    auto raise = [&](const f16v (&sc)[KB]) INLINE {
+        float top = sc[0][0];
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
+        top *= unit;
+        if (__any(top > ref + SLACK)) {
+            top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+            // (nothing is summed while ref is -inf but infinities, which no factor may turn into NaN)
+            const float now = fmaxf(ref, top), f = ref == -INFINITY ? 1.0f : fmaxf(weight_of(ref, now), 1e-37f);
+            ref = now;
+            sum *= f;
+#pragma unroll
+            for (int t = 0; t < ND; ++t) acc[t] *= f;
+        }
+    };
     // one tile: its keys and values lie at cur, the next tile's go to next
-    auto step = [&](int j, uint8_t* __restrict__ cur, uint8_t* __restrict__ next) {
+    auto step = [&](int j, uint8_t* __restrict__ cur, uint8_t* __restrict__ next) INLINE {
         wait_loads();
         __syncthreads();                           // tile j is there, and every wave is done with the other buffer
         const uint64_t ok = __ballot((unsigned)page < (unsigned)a.c.pages);
         if (j + TILE < to) {
-            load_tile(j + TILE, page_next, next);
+            load_tile(a.c.k, j + TILE, page_next, k_off, k_ok, next);
+            load_tile(a.c.v, j + TILE, page_next, v_off, v_ok, next + M::BYTES);
             page = page_next;
             page_next = page_of(j + 2 * TILE);
         }
@@ -784,44 +846,34 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
         }
         if (idle) return;                          // no row of this wave sees these keys
 
+        // (opaque here, so that the addresses made of them are not kept in registers)
+        int kb0 = k_base, vb0 = v_base;
+        asm volatile("" : "+v"(kb0), "+v"(vb0));
+        u4 kk[NK][KB];
+#pragma unroll
+        for (int c = 0; c < NK; ++c)
+#pragma unroll
+            for (int k = 0; k < KB; ++k)           // piece 2c + h of row 32 k + m: the permutation leaves an
+                kk[c][k] = *reinterpret_cast<const u4*>(cur + ((kb0 ^ (c * 32)) + k * 32 * ROW));      // exclusive or with 2c
         f16v sc[KB];
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            sc[k] = f16v{};
+        for (int k = 0; k < KB; ++k) sc[k] = f16v{};
 #pragma unroll
-            for (int c = 0; c < NK; ++c) {
-                // piece 2c + h of row 32 k + m: the permutation leaves an exclusive or with 2c
-                const u4 kk = *reinterpret_cast<const u4*>(cur + ((k_base ^ (c * 32)) + k * 32 * ROW));
+        for (int c = 0; c < NK; ++c) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
                 if constexpr (DT == F16) {
-                    sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kk), __builtin_bit_cast(h8, q[c]),
+                    sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kk[c][k]), __builtin_bit_cast(h8, q[c]),
                                                                    sc[k], 0, 0, 0);
                 } else {
-                    const f4 kf = __builtin_bit_cast(f4, kk), qf = __builtin_bit_cast(f4, q[c]);
+                    const f4 kf = __builtin_bit_cast(f4, kk[c][k]), qf = __builtin_bit_cast(f4, q[c]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(kf[e], qf[e], sc[k], 0, 0, 0);
                 }
             }
         }
-        // key of score r of block k: j + 32 k + 8 (r / 4) + 4 h + r % 4
         const bool whole = j >= in_lo && j + TILE <= in_hi && j + TILE <= to && pages;
-        if (RULES) {
-#pragma unroll
-            for (int k = 0; k < KB; ++k) sc[k] *= scale;
-            if (a.cap > 0.0f) {
-#pragma unroll
-                for (int k = 0; k < KB; ++k)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[k][r] = a.cap * LOG2E * tanh_of<DT>(sc[k][r]);
-            }
-            if (a.slopes) {
-                const float away = (float)(pos - j - 4 * h);
-#pragma unroll
-                for (int k = 0; k < KB; ++k)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r]);
-            }
-        }
+        by_rule(sc, j);
         if (!whole) {
             // seen: lo <= key < min(hi, to), as one unsigned comparison relative to this lane's first key
             const int at = lo - j - 4 * h;
@@ -841,52 +893,35 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
                             sc[k][r + i] = (ok >> (32 * k + 2 * r)) & 1 ? sc[k][r + i] : -INFINITY;
             }
         }
-        float top = sc[0][0];
-#pragma unroll
-        for (int k = 0; k < KB; ++k)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
-        const float unit = RULES ? 1.0f : scale;
-        top *= unit;
-        if (__any(top > ref + SLACK)) {
-            top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-            // (nothing is summed while ref is -inf but infinities, which no factor may turn into NaN)
-            const float now = fmaxf(ref, top), f = ref == -INFINITY ? 1.0f : fmaxf(weight_of(ref, now), 1e-37f);
-            ref = now;
-            sum *= f;
-#pragma unroll
-            for (int t = 0; t < ND; ++t) acc[t] *= f;
-        }
+        raise(sc);
         const float off = LIFT - (ref == -INFINITY ? 0.0f : ref);
         float part = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KB; ++k)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                sc[k][r] = __builtin_amdgcn_exp2f(fmaf(sc[k][r], unit, off));
-                part += sc[k][r];
-            }
-        sum += part;
-
         if constexpr (DT == F16) {
-            h8 p[2 * KB];                          // keys 16 n + {4 h + i, 8 + 4 h + i}
+            // V^T: elements 32 t + m of the keys 16 n + {4 h + i, 8 + 4 h + i} (rows 16 n + 4 h .. + 3, then 8
+            // further on, where the permutation is the same)
+            h8 v[ND][2 * KB];
 #pragma unroll
             for (int n = 0; n < 2 * KB; ++n)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[n][e] = (_Float16)sc[n / 2][8 * (n % 2) + e];
-            // V^T: elements 32 t + m of these keys (rows 16 n + 4 h .. + 3, then 8 further on, where the
-            // permutation is the same)
-            auto v_at = [&](int t, int n) {
-                const uint8_t* p0 = cur + ((v_base ^ (t * 64)) + M::BYTES + n * 16 * ROW);
-                const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p0);
-                const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(p0 + 8 * ROW));
-                return __builtin_bit_cast(h8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-            };
+                for (int t = 0; t < ND; ++t) {
+                    const uint8_t* p0 = cur + ((vb0 ^ (t * 64)) + M::BYTES + n * 16 * ROW);
+                    const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p0);
+                    const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(p0 + 8 * ROW));
+                    v[t][n] = __builtin_bit_cast(h8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+            h8 p[2 * KB];
 #pragma unroll
-            for (int t = 0; t < ND; ++t)
+            for (int n = 0; n < 2 * KB; ++n)
 #pragma unroll
-                for (int n = 0; n < 2 * KB; ++n)
-                    acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_at(t, n), p[n], acc[t], 0, 0, 0);
+                for (int e = 0; e < 8; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(fmaf(sc[n / 2][8 * (n % 2) + e], unit, off));
+                    part += w;
+                    p[n][e] = (_Float16)w;
+                }
+#pragma unroll
+            for (int n = 0; n < 2 * KB; ++n)
+#pragma unroll
+                for (int t = 0; t < ND; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[t][n], p[n], acc[t], 0, 0, 0);
         } else {
             // V: elements ND m .. ND m + ND - 1 of key 32 k + 8 (r / 4) + 4 h + r % 4
             typedef float vrow __attribute__((ext_vector_type(ND)));
@@ -898,11 +933,20 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const vrow v = v_at(k, r);
+                    const float w = __builtin_amdgcn_exp2f(fmaf(sc[k][r], unit, off));
+                    part += w;
 #pragma unroll
-                    for (int t = 0; t < ND; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[t], sc[k][r], acc[t], 0, 0, 0);
+                    for (int t = 0; t < ND; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[t], w, acc[t], 0, 0, 0);
                 }
         }
+        sum += part;
     };
+    if (from < to) {
+        page = page_of(from);
+        load_tile(a.c.k, from, page, k_off, k_ok, smem);
+        load_tile(a.c.v, from, page, v_off, v_ok, smem + M::BYTES);
+        page_next = page_of(from + TILE);
+    }
     for (int j = from; j < to; j += 2 * TILE) {
         step(j, smem, smem + 2 * M::BYTES);
         if (j + TILE < to) step(j + TILE, smem + 2 * M::BYTES, smem);
@@ -939,32 +983,54 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     }
 }
 
-// Join of a row's splits, in their order: four elements per thread.
-template <int DT>
-__global__ __launch_bounds__(WAVE) void k_attn_join(AttnArgs a) {
+// Join of a row's splits: four elements per thread, GROUPS threads for the same ones, each with every
+// GROUPS-th split; the order of the sums is fixed.
+template <int DT, int GROUPS>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    constexpr int PIECES = 256 / GROUPS;
+    __shared__ f4 po[256];
+    __shared__ float2 pml[256];
     const int flat = blockIdx.z, kvh = blockIdx.y, d = a.c.head_dim, pieces = d / 4;
     const int n = min(a.part_n[flat], a.splits);
     if (n <= 1) return;                           // written by the only one
     int s = flat, r0 = 0;
     if (a.rows > FEW_ROWS && !tile_at(a, flat, a.rows, a.most_rows, s, r0)) return;
     const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
-    const int i = blockIdx.x * WAVE + threadIdx.x, r = i / pieces, e = (i - r * pieces) * 4;
-    if (r >= min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)a.rows)) return;
+    const int g = threadIdx.x / PIECES;
+    const int i = blockIdx.x * PIECES + threadIdx.x % PIECES, r = i / pieces, e = (i - r * pieces) * 4;
+    const bool row = r < min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)a.rows);
     const int64_t at = ((int64_t)flat * a.c.kv_heads + kvh) * a.splits * a.rows + r;
     float top = -INFINITY, l = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) top = fmaxf(top, a.part_ml[at + (int64_t)k * a.rows].x);
     f4 o = f4{0, 0, 0, 0};
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-        const float2 ml = a.part_ml[at + (int64_t)k * a.rows];
-        const f4 v = *reinterpret_cast<const f4*>(a.part + (at + (int64_t)k * a.rows) * d + e);
+    auto add = [&](float2 ml, f4 v) INLINE {      // (a split that saw nothing holds no more than zeros)
         const float f = weight_of(ml.x, top);
-        l += f == 0.0f ? 0.0f : f * ml.y;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] += f == 0.0f ? 0.0f : f * v[c];
+        if (f == 0.0f) return;
+        l += f * ml.y;
+        o += f * v;
+    };
+    if (row) {
+#pragma unroll 4
+        for (int k = g; k < n; k += GROUPS) top = fmaxf(top, a.part_ml[at + (int64_t)k * a.rows].x);
+#pragma unroll 4
+        for (int k = g; k < n; k += GROUPS)
+            add(a.part_ml[at + (int64_t)k * a.rows], *reinterpret_cast<const f4*>(a.part + (at + (int64_t)k * a.rows) * d + e));
     }
-    store_row<DT>(a, t0 + (r0 + r) / a.group, kvh * a.group + (r0 + r) % a.group, e, o, top, l);
+    if (GROUPS > 1) {
+        po[threadIdx.x] = o;
+        pml[threadIdx.x] = make_float2(top, l);
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int k = 1; k < GROUPS; ++k) top = fmaxf(top, pml[threadIdx.x + k * PIECES].x);
+        const float2 first = make_float2(pml[threadIdx.x].x, l);
+        const f4 v = o;
+        l = 0.0f;
+        o = f4{0, 0, 0, 0};
+        add(first, v);
+#pragma unroll
+        for (int k = 1; k < GROUPS; ++k) add(pml[threadIdx.x + k * PIECES], po[threadIdx.x + k * PIECES]);
+    }
+    if (row) store_row<DT>(a, t0 + (r0 + r) / a.group, kvh * a.group + (r0 + r) % a.group, e, o, top, l);
 }
 
 }  // namespace pi

@@ -41,9 +41,9 @@ Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
         p.rows = (int)p.most_rows;
         split_keys(p, p.tiles * c->kv_heads, 2048, 256, b->max_len);
     } else {
+        p.rows = MANY_ROWS;
         p.tiles = std::min((int64_t)b->n_tokens * group / MANY_ROWS + b->n_seqs,
                            b->n_seqs * ((p.most_rows + MANY_ROWS - 1) / MANY_ROWS));
-        p.rows = MANY_ROWS;
         split_keys(p, p.tiles * c->kv_heads, 512, 512, b->max_len);
     }
     p.part = 0;
@@ -54,12 +54,18 @@ Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
     return p;
 }
 
+template <int DT, int GROUPS>
+pi_status launch_join_by(const AttnArgs& a, hipStream_t s) {
+    const int pieces = a.rows * (a.c.head_dim / 4), per = 256 / GROUPS;
+    return launch(PI_K_ATTN_JOIN, k_attn_join<DT, GROUPS>, dim3((pieces + per - 1) / per, a.c.kv_heads, a.tiles), dim3(256), 0,
+                  s, a);
+}
+
 template <int DT>
 pi_status launch_join(const AttnArgs& a, hipStream_t s) {
     if (a.splits == 1) return PI_OK;
-    const int pieces = a.rows * (a.c.head_dim / 4);
-    return launch(PI_K_ATTN_JOIN, k_attn_join<DT>, dim3((pieces + WAVE - 1) / WAVE, a.c.kv_heads, a.tiles), dim3(WAVE),
-                  0, s, a);
+    // one thread's loads of many splits would wait for each other
+    return a.splits <= 8 ? launch_join_by<DT, 1>(a, s) : launch_join_by<DT, 16>(a, s);
 }
 
 template <int DT, int DP, bool FULL>
