@@ -22,8 +22,8 @@ struct Plan {
     size_t part, ml, n, bytes; // offsets in the workspace, its size
 };
 
-// Keys per split so that about `want` workgroups have work when every sequence is max_len long;
-// none smaller than `least` keys (the join costs as much as reading some hundred keys).
+// Keys per split so that about `want` workgroups have work when every sequence is max_len long (`alone`: without
+// splits); none smaller than `least` keys.
 void split_keys(Plan& p, int64_t alone, int64_t want, int64_t least, int max_len) {
     const int64_t n = std::max<int64_t>(1, want / std::max<int64_t>(1, alone));
     const int64_t chunk = std::max<int64_t>(least, ((int64_t)max_len + n - 1) / n);
@@ -39,12 +39,22 @@ Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
     if (p.few) {
         p.tiles = b->n_seqs;
         p.rows = (int)p.most_rows;
-        split_keys(p, p.tiles * c->kv_heads, 2048, 256, b->max_len);
+        // The chip holds 512 workgroups.  Few sequences are about alike, so two rounds do (one of 131072 tokens
+        // with 8 key heads: 89 us for 1024 workgroups, 97 for 2048, 105 for 3072); the lengths of many differ, and
+        // smaller pieces even them out (48 of 300 to 8191: 133, 104 and 94 us).  Up to 512 keys one workgroup is
+        // faster than two and the join (8.5 against 10.5 us).
+        const int64_t want = b->n_seqs <= 4 ? 1024 : b->n_seqs <= 16 ? 2048 : 3072;
+        split_keys(p, p.tiles * c->kv_heads, want, b->max_len <= 512 ? 512 : 256, b->max_len);
     } else {
         p.rows = MANY_ROWS;
         p.tiles = std::min((int64_t)b->n_tokens * group / MANY_ROWS + b->n_seqs,
                            b->n_seqs * ((p.most_rows + MANY_ROWS - 1) / MANY_ROWS));
-        split_keys(p, p.tiles * c->kv_heads, 512, 512, b->max_len);
+        // f16: 128 rows over 1000 keys take 17.5 us in pieces of 256 keys, 24 in pieces of 512; over 131072 keys 120 us
+        // for 512 workgroups, 142 for 1024.  A step of an f32 tile takes four times as long, so smaller pieces pay:
+        // 64 rows over 500 keys 26 us in pieces of 128, 35 of 256, 50 unsplit; over 16000 keys 80 us for 1024
+        // workgroups, 85 for 512.
+        const bool f32 = c->dtype == PI_F32;
+        split_keys(p, p.tiles * c->kv_heads, f32 ? 1024 : 512, f32 ? 128 : 256, b->max_len);
     }
     p.part = 0;
     const size_t slots = p.splits > 1 ? (size_t)p.tiles * c->kv_heads * p.splits * p.rows : 0;
@@ -65,14 +75,16 @@ template <int DT>
 pi_status launch_join(const AttnArgs& a, hipStream_t s) {
     if (a.splits == 1) return PI_OK;
     // one thread's loads of many splits would wait for each other
-    return a.splits <= 8 ? launch_join_by<DT, 1>(a, s) : launch_join_by<DT, 16>(a, s);
+    return a.splits <= 4    ? launch_join_by<DT, 1>(a, s)
+           : a.splits <= 24 ? launch_join_by<DT, 4>(a, s)
+                            : launch_join_by<DT, 16>(a, s);
 }
 
 template <int DT, int DP, bool FULL>
 pi_status launch_few(const AttnArgs& a, hipStream_t s) {
     auto kern = k_attn_few<DT, DP, FULL>;
     TRY(allow_lds(kern, few_lds<DP>()));
-    TRY(launch(PI_K_ATTN, kern, dim3(a.splits, a.c.kv_heads, a.b.n_seqs), dim3(WAVE * FEW_WAVES), few_lds<DP>(), s, a));
+    TRY(launch(PI_K_ATTN, kern, dim3(a.c.kv_heads, a.splits, a.b.n_seqs), dim3(WAVE * FEW_WAVES), few_lds<DP>(), s, a));
     return launch_join<DT>(a, s);
 }
 

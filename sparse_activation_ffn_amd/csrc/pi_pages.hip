@@ -237,14 +237,21 @@ __device__ __forceinline__ int64_t block_excl_scan64(int64_t v, int64_t* lds, in
 
 // refs of the PER pages from p on (1 past the end: not free)
 __device__ __forceinline__ void load_refs(const int* refs, int pages, int p, int r[PER]) {
+    if (p + PER <= pages && reinterpret_cast<uintptr_t>(refs) % 16 == 0) {   // p is a multiple of PER
 #pragma unroll
-    for (int e = 0; e < PER; ++e) r[e] = p + e < pages ? refs[p + e] : 1;
+        for (int e = 0; e < PER; e += 4) {
+            const u4 w = *reinterpret_cast<const u4*>(refs + p + e);
+            r[e] = w.x, r[e + 1] = w.y, r[e + 2] = w.z, r[e + 3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) r[e] = p + e < pages ? refs[p + e] : 1;
+    }
 }
 
 // Needs, grants and page numbers of a call of pi_pages_extend, one workgroup: a
 // scan over the sequences' needs, then over the counts for the lowest free
-// pages, which ends as soon as enough are found; then a wave per sequence
-// writes its table entries.
+// pages, which ends as soon as enough are found; then the tables' entries.
 __global__ __launch_bounds__(PT) void k_pages_extend(pi_page_state st, const int* seqs, const int* add, int n,
                                                      int* granted, int* copies, int* start, int* free_ids) {
     __shared__ int lds[PT / WAVE];
@@ -298,32 +305,46 @@ __global__ __launch_bounds__(PT) void k_pages_extend(pi_page_state st, const int
     }
     __threadfence_block();
     __syncthreads();
-    // 3. grants and table entries
-    const int wave = tid / WAVE, lane = tid % WAVE;
-    for (int i = wave; i < n; i += PT / WAVE) {
-        const int from = start[i], need = granted[i], last = copies[i];
-        const bool ok = from >= 0 && (int64_t)from + need <= found;
-        int fresh = -1;
-        if (ok) {
-            const int s = seqs[i], a = add[i], len = st.lens[s];
-            const int have = (int)(((int64_t)len + st.page_size - 1) >> shift);
-            const int begin = have - (last >= 0);
-            int* row = st.table + (int64_t)s * st.table_stride;
-            for (int e = lane; e < need && begin + e < st.table_stride; e += WAVE) {
-                const int p = free_ids[from + e];
-                row[begin + e] = p;
-                st.refs[p] = 1;
+    // 3. grants and table entries: a thread per sequence, and the whole wave for one that takes many pages
+    constexpr int FEW = 4;
+    const int lane = tid % WAVE;
+    for (int base = 0; base < n; base += PT) {
+        const int i = base + tid;
+        int s = 0, from = 0, begin = 0, need = 0;
+        bool ok = false;
+        if (i < n) {
+            from = start[i];
+            need = granted[i];
+            const int last = copies[i];
+            ok = from >= 0 && (int64_t)from + need <= found;
+            int fresh = -1;
+            if (ok) {
+                s = seqs[i];
+                const int len = st.lens[s];
+                begin = (int)(((int64_t)len + st.page_size - 1) >> shift) - (last >= 0);
+                st.lens[s] = len + add[i];
+                if (last >= 0) {
+                    atomicSub(&st.refs[last], 1);
+                    fresh = free_ids[from];
+                }
             }
-            if (last >= 0) fresh = free_ids[from];
-            if (lane == 0) {
-                if (last >= 0) atomicSub(&st.refs[last], 1);
-                st.lens[s] = len + a;
-            }
-        }
-        if (lane == 0) {
             granted[i] = ok;
             copies[i] = ok ? last : -1;
             copies[n + i] = fresh;
+        }
+        int* row = st.table + (int64_t)s * st.table_stride;
+        auto take = [&](int* row, int begin, int from, int e) {
+            const int p = free_ids[from + e];
+            if (begin + e < st.table_stride) row[begin + e] = p;
+            st.refs[p] = 1;
+        };
+        if (ok && need <= FEW)
+            for (int e = 0; e < need; ++e) take(row, begin, from, e);
+        for (uint64_t many = __ballot(ok && need > FEW); many; many &= many - 1) {
+            const int k = __builtin_ctzll(many);
+            int* r = st.table + (int64_t)__shfl(s, k, WAVE) * st.table_stride;
+            const int b0 = __shfl(begin, k, WAVE), f0 = __shfl(from, k, WAVE), m = __shfl(need, k, WAVE);
+            for (int e = lane; e < m; e += WAVE) take(r, b0, f0, e);
         }
     }
 }
