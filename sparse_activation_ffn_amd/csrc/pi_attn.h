@@ -70,12 +70,10 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - LIFT + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-// tanh for the cap on scores.  1 - 2 / (e^2y + 1) is within 2^-22 of it (absolute); for 32-bit caches the
-// library's, whose relative error is that small
-template <int DT>
-__device__ __forceinline__ float tanh_of(float y) {
-    if (DT == F32) return tanhf(y);
-    return 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * LOG2E * y) + 1.0f);
+// cap tanh(x) with 2 x log2 e = s twice, as cap (1 - 2 / (e^2x + 1)): within cap 2^-22 (absolute).  For 32-bit
+// caches the kernels call tanhf, whose relative error is that small.
+__device__ __forceinline__ float capped(float s, float twice, float cap) {
+    return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * twice) + 1.0f), cap);
 }
 
 template <int DT> struct ElemT;
@@ -304,7 +302,8 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
             for (int i = 0; i < 4; ++i) {
                 const int key = j + 16 * u + 4 * g + i;
                 float v = sc[u][i] * scale;
-                if (a.cap > 0.0f) v = a.cap * LOG2E * tanh_of<DT>(v);
+                if (a.cap > 0.0f)
+                    v = DT == F16 ? capped(v, 2.0f * LOG2E, a.cap * LOG2E) : a.cap * LOG2E * tanhf(v);
                 if (a.slopes) v -= slope * (float)abs(pos - key);
                 sees[u][i] = true;
                 if (!whole) {
@@ -781,24 +780,26 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     int page = 0, page_next = 0;
 
     // cap and bias of the scores of tile j; score r of block k belongs to key j + 32 k + 8 (r / 4) + 4 h + r % 4
+    const float cap = a.cap * LOG2E, twice = 2.0f * LOG2E * scale;
     auto by_rule = [&](f16v (&sc)[KB], int j) INLINE {
-        if (RULES) {
+        if (!RULES) return;
+        if (a.cap > 0.0f) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    sc[k][r] = DT == F16 ? capped(sc[k][r], twice, cap) : cap * tanhf(sc[k][r] * scale);
+        } else {
 #pragma unroll
             for (int k = 0; k < KB; ++k) sc[k] *= scale;
-            if (a.cap > 0.0f) {
+        }
+        if (a.slopes) {
+            const float away = (float)(pos - j - 4 * h);
 #pragma unroll
-                for (int k = 0; k < KB; ++k)
+            for (int k = 0; k < KB; ++k)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[k][r] = a.cap * LOG2E * tanh_of<DT>(sc[k][r]);
-            }
-            if (a.slopes) {
-                const float away = (float)(pos - j - 4 * h);
-#pragma unroll
-                for (int k = 0; k < KB; ++k)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r]);
-            }
+                for (int r = 0; r < 16; ++r)
+                    sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r]);
         }
     };
     // moves the reference when a score passes it by too much

@@ -31,8 +31,11 @@ void split_keys(Plan& p, int64_t alone, int64_t want, int64_t least, int max_len
     p.splits = std::max(1, (int)(((int64_t)max_len + p.chunk - 1) / p.chunk));
 }
 
-Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
+// rule NULL: a plan for the rule that needs most
+Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads, const pi_score_rule* rule) {
     Plan p{};
+    // keys that the rows of one sequence span
+    const int span = rule && rule->window > 0 ? (int)std::min<int64_t>(b->max_len, (int64_t)rule->window + b->max_new) : b->max_len;
     const int group = q_heads / c->kv_heads;
     p.most_rows = (int64_t)std::min(b->max_new, b->n_tokens) * group;
     p.few = p.most_rows <= FEW_ROWS;
@@ -44,18 +47,24 @@ Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads) {
         // smaller pieces even them out (48 of 300 to 8191: 133, 104 and 94 us).  Up to 512 keys one workgroup is
         // faster than two and the join (8.5 against 10.5 us).
         const int64_t want = b->n_seqs <= 4 ? 1024 : b->n_seqs <= 16 ? 2048 : 3072;
-        split_keys(p, p.tiles * c->kv_heads, want, b->max_len <= 512 ? 512 : 256, b->max_len);
+        split_keys(p, p.tiles * c->kv_heads, want, span <= 512 ? 512 : 256, span);
     } else {
         p.rows = MANY_ROWS;
         p.tiles = std::min((int64_t)b->n_tokens * group / MANY_ROWS + b->n_seqs,
                            b->n_seqs * ((p.most_rows + MANY_ROWS - 1) / MANY_ROWS));
-        // f16: 128 rows over 1000 keys take 17.5 us in pieces of 256 keys, 24 in pieces of 512; over 131072 keys 120 us
-        // for 512 workgroups, 142 for 1024.  A step of an f32 tile takes four times as long, so smaller pieces pay:
-        // 64 rows over 500 keys 26 us in pieces of 128, 35 of 256, 50 unsplit; over 16000 keys 80 us for 1024
-        // workgroups, 85 for 512.
-        const bool f32 = c->dtype == PI_F32;
-        split_keys(p, p.tiles * c->kv_heads, f32 ? 1024 : 512, f32 ? 128 : 256, b->max_len);
+        // One sequence: its tiles are about alike.  f16: 128 rows over 1000 keys take 17.5 us in pieces of 256 keys, 24
+        // in pieces of 512; over 131072 keys 120 us for 512 workgroups, 142 for 1024.  A step of an f32 tile takes four
+        // times as long, so smaller pieces pay: 64 rows over 500 keys 26 us in pieces of 128, 35 of 256, 50 unsplit;
+        // over 16000 keys 80 us for 1024 workgroups, 85 for 512.
+        // Several: the tiles of the longest would be left alone at the end, so they are split further, but not under
+        // 2048 keys where there are enough without (8 sequences of 100 to 8000 tokens, 1024 to 1 of them new: 180 us for
+        // 512 workgroups, 113 for 2048, 174 for 4096; all 8 of 8000: 531 us against 555).
+        const bool f32 = c->dtype == PI_F32, several = !f32 && b->n_seqs > 1;
+        const int64_t alone = p.tiles * c->kv_heads;
+        split_keys(p, alone, f32 ? 1024 : several ? 2048 : 512, f32 ? 128 : several && alone >= 512 ? 2048 : 256, span);
     }
+    // (a shorter span never takes more workspace)
+    if (rule) p.splits = std::min(p.splits, plan_attention(c, b, q_heads, nullptr).splits);
     p.part = 0;
     const size_t slots = p.splits > 1 ? (size_t)p.tiles * c->kv_heads * p.splits * p.rows : 0;
     p.ml = align256(slots * c->head_dim * 4);
@@ -129,7 +138,7 @@ extern "C" {
 
 size_t pi_attention_workspace_bytes(const pi_kv_cache* cache, const pi_seq_batch* batch, int32_t q_heads) {
     if (check_cache(cache) != PI_OK || check_batch(batch) != PI_OK || check_q_heads(cache, q_heads) != PI_OK) return 0;
-    return plan_attention(cache, batch, q_heads).bytes;
+    return plan_attention(cache, batch, q_heads, nullptr).bytes;
 }
 
 pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_seq_batch* batch,
@@ -146,7 +155,7 @@ pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_s
     if (batch->n_seqs == 0 || batch->n_tokens == 0) return PI_OK;
     TRY(check_rows(q, "q", cache->dtype));
     TRY(check_rows(out, "out", cache->dtype));
-    const Plan p = plan_attention(cache, batch, q_heads);
+    const Plan p = plan_attention(cache, batch, q_heads, rule);
     CHECK(ws, PI_ERR_WORKSPACE, "workspace is NULL");
     CHECK(aligned(ws, 256), PI_ERR_ALIGN, "workspace must be 256-byte aligned");
     CHECK(ws_bytes >= p.bytes, PI_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p.bytes);
