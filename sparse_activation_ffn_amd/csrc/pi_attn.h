@@ -160,7 +160,7 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
 
     const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
     const int len = clamped_len(a.b, shift, s), q_end = a.b.q_start[s + 1];
-    const int n_rows = min((t1 - t0) * a.group, a.rows);
+    const int n_rows = (int)min((int64_t)(t1 - t0) * a.group, (int64_t)a.rows);
     if (n_rows <= 0) return;
 
     // this lane's row, and the keys it sees; lanes without a row see whatever the others do

@@ -22,6 +22,8 @@ struct Plan {
     size_t part, ml, n, bytes; // offsets in the workspace, its size
 };
 
+constexpr int64_t MAX_ITEMS = 1 << 23;   // workgroups of a launch: 2^31 threads
+
 // Keys per split so that about `want` workgroups have work when every sequence is max_len long (`alone`: without
 // splits); none smaller than `least` keys.
 void split_keys(Plan& p, int64_t alone, int64_t want, int64_t least, int max_len) {
@@ -101,9 +103,7 @@ template <int DT, int DP, bool FULL, bool RULES>
 pi_status launch_many(const AttnArgs& a, hipStream_t s) {
     auto kern = k_attn_many<DT, DP, FULL, RULES>;
     TRY(allow_lds(kern, many_lds<DT, DP>()));
-    const int64_t items = (int64_t)a.tiles * a.c.kv_heads * a.splits;
-    CHECK(items <= 1 << 23, PI_ERR_SHAPE, "too many rows for one call (%lld tiles of %d)", (long long)items, MANY_ROWS);
-    const int grid = (int)((items + XCDS - 1) / XCDS * XCDS);
+    const int grid = (a.tiles * a.c.kv_heads * a.splits + XCDS - 1) / XCDS * XCDS;
     TRY(launch(PI_K_ATTN, kern, dim3(grid), dim3(WAVE * MANY_WAVES), many_lds<DT, DP>(), s, a));
     return launch_join<DT>(a, s);
 }
@@ -160,6 +160,7 @@ pi_status pi_paged_attention(const pi_kv_cache* cache, int32_t layer, const pi_s
     CHECK(aligned(ws, 256), PI_ERR_ALIGN, "workspace must be 256-byte aligned");
     CHECK(ws_bytes >= p.bytes, PI_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p.bytes);
     if (batch->max_new == 0) return PI_OK;
+    CHECK(p.tiles * cache->kv_heads * p.splits <= MAX_ITEMS, PI_ERR_SHAPE, "too many rows for one call");
     AttnArgs a{};
     a.c = cache_layer(cache, layer);
     a.b = seq_batch(batch);
