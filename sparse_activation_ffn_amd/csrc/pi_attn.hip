@@ -46,10 +46,14 @@ Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads, co
         p.rows = (int)p.most_rows;
         // The chip holds 512 workgroups.  Few sequences are about alike, so two rounds do (one of 131072 tokens
         // with 8 key heads: 89 us for 1024 workgroups, 97 for 2048, 105 for 3072); the lengths of many differ, and
-        // smaller pieces even them out (48 of 300 to 8191: 133, 104 and 94 us).  Up to 512 keys one workgroup is
-        // faster than two and the join (8.5 against 10.5 us).
-        const int64_t want = b->n_seqs <= 4 ? 1024 : b->n_seqs <= 16 ? 2048 : 3072;
-        split_keys(p, p.tiles * c->kv_heads, want, span <= 512 ? 512 : 256, span);
+        // smaller pieces even them out (48 of 300 to 8191: 133, 104 and 94 us).
+        const int64_t want = b->n_seqs <= 4 ? 1024 : b->n_seqs <= 16 ? 2048 : 3072, alone = p.tiles * c->kv_heads;
+        // A workgroup takes 3 to 4 us before its first key, the join 4: one piece up to 128 KB of keys (500 keys of 128
+        // f16: 10.5 us against 12.3 in two), and the more workgroups there are, the longer the pieces (1000 keys,
+        // 512 workgroups: 43 us, in pieces of 256 53; 64 workgroups 14.6 and 12.5).
+        const bool small = (int64_t)span * c->head_dim * dtype_size(c->dtype) <= 128 << 10;
+        const int least = small ? std::max(span, 1) : alone <= 128 ? 256 : alone <= 256 ? 512 : 1024;
+        split_keys(p, alone, want, least, span);
     } else {
         p.rows = MANY_ROWS;
         p.tiles = std::min((int64_t)b->n_tokens * group / MANY_ROWS + b->n_seqs,
