@@ -25,6 +25,8 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // HBM rate bounds it (a launch, for single tokens).  The angles of a token are
 // the same for all its heads: a workgroup takes one token (and a slice of its
 // heads), forms each angle's sin and cos once and keeps them in LDS.
+// Measured: 8192 tokens, 128 query and 8 key heads of 64 f16: 60 us, 5.0 TB/s (a
+// copy of 2 GB: 4.9); 64 tokens, 64 and 8 heads of 128: 3.6 us.
 constexpr int RT = 256;
 
 struct RopeArgs {
@@ -252,6 +254,9 @@ __device__ __forceinline__ void load_refs(const int* refs, int pages, int p, int
 // Needs, grants and page numbers of a call of pi_pages_extend, one workgroup: a
 // scan over the sequences' needs, then over the counts for the lowest free
 // pages, which ends as soon as enough are found; then the tables' entries.
+// One workgroup because every step needs the sums of the one before; bound by
+// its chain of loads (list, length, table, count): 6 to 7.5 us for 128 to 205
+// sequences in pools of 10007 to 16384 pages.
 __global__ __launch_bounds__(PT) void k_pages_extend(pi_page_state st, const int* seqs, const int* add, int n,
                                                      int* granted, int* copies, int* start, int* free_ids) {
     __shared__ int lds[PT / WAVE];
@@ -350,7 +355,8 @@ __global__ __launch_bounds__(PT) void k_pages_extend(pi_page_state st, const int
 }
 
 // Page copies: pair i (src, dst) of every layer, k and v.  A page of one layer is
-// one contiguous block; a workgroup takes pieces of it of COPY_BYTES.
+// one contiguous block; a workgroup takes pieces of it of COPY_BYTES.  Bound by
+// HBM: 47 MB read and written in 8.4 us, 420 MB in 87 us (4.8 TB/s).
 constexpr int CT = 256;
 constexpr int COPY_BYTES = CT * 16 * 4;
 
