@@ -572,11 +572,12 @@ typedef struct pi_score_rule {
  * h reads key head h / (q_heads / kv_heads).
  *   out[t][h] = sum_j w_j V[j] / sum_j w_j,  w_j = exp(score_j - max)
  *   lse[t][h] (float32 [n_tokens][q_heads], or NULL) = max + ln sum_j w_j
- * A row that sees no key gets zeros and lse = -inf.  Keys that a row does not
- * see have no influence on it, whatever they hold (infinities and NaN
- * included).  Scores, weights, sums and outputs are float32 until the output is
- * rounded once; with PI_F16 the weights are rounded to f16 for the product with
- * V (relative error 2^-12 each), their sum is not.  out may be q.
+ * A row that sees no key, or only scores of -inf, gets zeros and lse = -inf.
+ * Keys that a row does not see have no influence on it, whatever they hold
+ * (infinities and NaN included).  Scores, weights, sums and outputs are float32
+ * until the output is rounded once; with PI_F16 the weights are rounded to f16
+ * for the product with V (relative error 2^-12 each), their sum is not.  out may
+ * be q.
  * Needs a workspace of pi_attention_workspace_bytes (256-byte aligned).
  */
 size_t pi_attention_workspace_bytes(const pi_kv_cache* cache, const pi_seq_batch* batch,

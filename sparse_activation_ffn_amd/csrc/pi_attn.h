@@ -52,13 +52,14 @@ struct AttnArgs {
     int* part_n;                      // [tiles]: splits that hold something
 };
 
-// keys that row t at position pos of sequence s sees
+// keys that row t at position pos of sequence s sees: 0 <= lo <= hi <= len (lo == hi: none), whatever the bounds given
 __device__ __forceinline__ void visible(const AttnArgs& a, int t, int pos, int s, int len, int& lo, int& hi) {
-    lo = a.first ? max(a.first[t], 0) : 0;
-    if (a.window > 0) lo = max(lo, pos - a.window + 1);
     hi = pos + 1;
     if (a.prefix) hi = max(hi, a.prefix[s]);
-    hi = min(hi, len);
+    hi = max(min(hi, len), 0);
+    lo = a.first ? max(a.first[t], 0) : 0;
+    if (a.window > 0 && pos >= a.window) lo = max(lo, pos - a.window + 1);
+    lo = min(lo, hi);
 }
 
 // weight of a sum taken against reference m, seen from reference top (-inf: nothing was summed)
@@ -218,7 +219,8 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
         for (int i = 0; i < 2 * U; ++i) r.p[i] = table[min((j + 8 * i) >> shift, last_page)];
         return r;
     };
-    // byte offset of key j + i (i in the 8 keys `eight` of the step); a page that is none reads page 0, masked
+    // byte offset of key j of step u (`second`: in the step's second 8 keys, whose page may be another); a page that is
+    // none reads page 0, masked
     auto row_at = [&](const Pages& r, int u, bool second, int j) {
         const int p0 = r.p[2 * u], p1 = r.p[2 * u + 1];
         int p = second ? p1 : p0;

@@ -149,6 +149,19 @@ def test_attention_rows_that_see_nothing(dtype, new):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 70, 9]])
+def test_attention_extreme_bounds(dtype, new):
+    """Windows, prefixes and first keys at the ends of 32 bits, for rows before position 0 too."""
+    c = Case(dtype, 4, 2, 64, 16, new, [20, 200, 3], seed=15)
+    top = 2 ** 31 - 1
+    for window in (top, 1, 0):
+        for prefix in ([top, 10, 2], [-top - 1, -5, 1]):
+            first = np.array([(-top - 1, 0, 5, top)[t % 4] for t in range(c.T)])
+            c.run(window=window, prefix=np.array(prefix))
+            c.run(window=window, prefix=np.array(prefix), first=first)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("new", [1, 90])
 @pytest.mark.parametrize("d", [64, 80, 128, 256])
 def test_attention_masked_values_have_no_influence(dtype, new, d):
