@@ -11,6 +11,7 @@
 // most 2^14, and small ones stay clear of f16's subnormals (they lose bits below
 // 2^-20 of the largest one).
 #pragma once
+#include <algorithm>
 #include <type_traits>
 
 #include "pi_cache.h"
@@ -71,11 +72,27 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - LIFT + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-// cap tanh(x) with 2 x log2 e = s twice, as cap (1 - 2 / (e^2x + 1)): within cap 2^-22 (absolute).  For 32-bit
-// caches the kernels call tanhf, whose relative error is that small.
-__device__ __forceinline__ float capped(float s, float twice, float cap) {
-    return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(s * twice) + 1.0f), cap);
+// Capped scores are cap tanh(x), x = scale q.k / cap.  f32 caches: tanhf.  f16 caches: for |x| <= 3/4 x times a quartic in
+// x^2 (its coefficients are those of the least largest relative error, 6e-7, found by weighted least squares), else
+// 1 - 2 / (e^2x + 1), which is within 2^-22 and so within 1e-6 of the value there, but not for small x.
+constexpr float TANH_SMALL = 0.75f;
+
+constexpr float TANH_C[5] = {0.99999943f, -0.33328252f, 0.13258983f, -0.05005630f, 0.01292963f};
+__device__ __forceinline__ float odd_poly(float x, float c1, float c3, float c5, float c7, float c9) {
+    const float u = x * x;
+    return x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, c9, c7), c5), c3), c1);
 }
+
+template <int DT>
+__device__ __forceinline__ float tanh_of(float x) {
+    if (DT == F32) return tanhf(x);
+    const float big = fmaf(-2.0f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * (2.0f * LOG2E)) + 1.0f), 1.0f);
+    return fabsf(x) <= TANH_SMALL ? odd_poly(x, TANH_C[0], TANH_C[1], TANH_C[2], TANH_C[3], TANH_C[4]) : big;
+}
+
+// scale / cap and cap log2 e, kept finite so that a product q.k of 0 stays 0
+__device__ __forceinline__ float cap_rate(float scale, float cap) { return fmaxf(-3e38f, fminf(scale / cap, 3e38f)); }
+__device__ __forceinline__ float cap_unit(float cap) { return fminf(cap, 2e38f) * LOG2E; }
 
 template <int DT> struct ElemT;
 template <> struct ElemT<F32> { typedef float T; typedef f4 V4; };
@@ -144,19 +161,16 @@ __device__ __forceinline__ unsigned nonfinite_h2(unsigned w) {
     return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
+// Split sp of rows r0 and on (16 at most are there) of sequence s and key head kvh, by the whole workgroup;
+// `flat` is the tile's place in the workspace.
 template <int DT, int DP, bool FULL>
-__global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1) void k_attn_few(AttnArgs a) {
+__device__ __forceinline__ void few_rows(const AttnArgs& a, int s, int r0, int kvh, int sp, int flat, float* lds) {
     typedef Few<DT, DP> F;
     constexpr int STEP = F::STEP, U = STEP / 16, EV = F::EV, VW = F::VW;
     constexpr int NK = DP / (4 * EV);              // 16-byte pieces of a key per lane
     constexpr int NV = DP / (16 * VW);             // pieces of a value row per lane
     constexpr int ES = 16 / EV;                    // bytes per element
-    extern __shared__ float lds[];
 
-    // Workgroups go round the XCDs.  Heads vary fastest, and the order of the splits turns with the sequence:
-    // short sequences have no late splits, and the XCD that got only those would be idle (48 sequences of
-    // 300 to 8191 tokens, 8 splits: 179 us with splits fastest, 101 us with 5 splits).
-    const int s = blockIdx.z, kvh = blockIdx.x, sp = (blockIdx.y + blockIdx.z) % a.splits;
     const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int m = lane % 16, g = lane / 16;
     const int d = FULL ? DP : a.c.head_dim;
@@ -164,11 +178,11 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
 
     const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
     const int len = clamped_len(a.b, shift, s), q_end = a.b.q_start[s + 1];
-    const int n_rows = (int)min((int64_t)(t1 - t0) * a.group, (int64_t)a.rows);
+    const int n_rows = (int)min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)FEW_ROWS);
     if (n_rows <= 0) return;
 
     // this lane's row, and the keys it sees; lanes without a row see whatever the others do
-    const int tok = t0 + m / a.group, head = kvh * a.group + m % a.group;
+    const int tok = t0 + (r0 + m) / a.group, head = kvh * a.group + (r0 + m) % a.group;
     const bool row = m < n_rows;
     int lo = 0, hi = 0x7fffffff, pos = 0;
     if (row) {
@@ -191,7 +205,7 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
     if (end == 0) start = 0;
     const int n_split = active_splits(a, start, end);
     if (sp >= n_split) return;
-    if (a.splits > 1 && sp == 0 && kvh == 0 && threadIdx.x == 0) a.part_n[s] = n_split;
+    if (a.splits > 1 && sp == 0 && kvh == 0 && threadIdx.x == 0) a.part_n[flat] = n_split;
     const int from = start + sp * a.chunk;
     const int to = sp == n_split - 1 ? end : from + a.chunk;
 
@@ -204,7 +218,7 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
         if (row && (FULL || e < d)) q[c] = ld16(a.q + (tok * a.q_ts + head * a.q_hs + e) * ES);
     }
     const float slope = a.slopes && row ? a.slopes[head] * LOG2E : 0.0f;
-    const float scale = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
+    const float scale = a.cap > 0.0f ? cap_rate(a.scale, a.cap) : a.scale * LOG2E;
 
     const int* table = a.b.table + (int64_t)s * a.b.table_stride;
     const int last_page = (len - 1) >> shift;
@@ -307,8 +321,7 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
             for (int i = 0; i < 4; ++i) {
                 const int key = j + 16 * u + 4 * g + i;
                 float v = sc[u][i] * scale;
-                if (a.cap > 0.0f)
-                    v = DT == F16 ? capped(v, 2.0f * LOG2E, a.cap * LOG2E) : a.cap * LOG2E * tanhf(v);
+                if (a.cap > 0.0f) v = cap_unit(a.cap) * tanh_of<DT>(v);
                 if (a.slopes) v -= slope * (float)abs(pos - key);
                 sees[u][i] = true;
                 if (!whole) {
@@ -483,13 +496,22 @@ __global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1)
             o += f * *reinterpret_cast<const f4*>(o_lds + (w * FEW_ROWS + r) * LD + e);
         }
         if (n_split > 1) {
-            const int64_t at = (((int64_t)s * a.c.kv_heads + kvh) * a.splits + sp) * a.rows + r;
+            const int64_t at = (((int64_t)flat * a.c.kv_heads + kvh) * a.splits + sp) * a.rows + r;
             *reinterpret_cast<f4*>(a.part + at * d + e) = o;
             if (e == 0) a.part_ml[at] = make_float2(all, l);
         } else {
-            store_row<DT>(a, t0 + r / a.group, kvh * a.group + r % a.group, e, o, all, l);
+            store_row<DT>(a, t0 + (r0 + r) / a.group, kvh * a.group + (r0 + r) % a.group, e, o, all, l);
         }
     }
+}
+
+template <int DT, int DP, bool FULL>
+__global__ __launch_bounds__(WAVE * FEW_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1) void k_attn_few(AttnArgs a) {
+    extern __shared__ float lds[];
+    // Workgroups go round the XCDs.  Heads vary fastest, and the order of the splits turns with the sequence:
+    // short sequences have no late splits, and the XCD that got only those would be idle (48 sequences of
+    // 300 to 8191 tokens, 8 splits: 179 us with splits fastest, 101 us with 5 splits).
+    few_rows<DT, DP, FULL>(a, blockIdx.z, 0, blockIdx.x, (blockIdx.y + blockIdx.z) % a.splits, blockIdx.z, lds);
 }
 
 // ---- many rows: chunks of new tokens -----------------------------------------------
@@ -527,7 +549,10 @@ template <int DT, int DP> struct Many {
     static constexpr int BYTES = TILE * ROW;
 };
 
-template <int DT, int DP> constexpr size_t many_lds() { return 4 * Many<DT, DP>::BYTES; }   // K and V, two buffers each
+// K and V, two buffers each (f32 tiles of few rows: their join)
+template <int DT, int DP> constexpr size_t many_lds() {
+    return std::max(4 * (size_t)Many<DT, DP>::BYTES, DT == F32 ? few_lds<DP>() : 0);
+}
 
 // piece c of row r of a K tile: 16 rows in a row at the same c read 16 different pieces of 256 bytes
 template <int ROW>
@@ -642,7 +667,7 @@ __device__ __forceinline__ void add_nonfinite(f16v* acc, const uint8_t* vt, int 
 
 // RULES: scores may be capped or biased (else they are scale * q.k alone)
 template <int DT, int DP, bool FULL, bool RULES>
-__global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a) {
+__global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1) void k_attn_many(AttnArgs a) {
     typedef Many<DT, DP> M;
     constexpr int TILE = M::TILE, ES = M::ES, ROW = M::ROW, KB = TILE / 32;
     constexpr int EV = 16 / ES, NC = ROW / 16;     // elements per piece, pieces per row
@@ -672,6 +697,16 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
     const int len = clamped_len(a.b, shift, s), q_end = a.b.q_start[s + 1];
     const int n_rows = (int)min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)MANY_ROWS);
+
+    // In an f32 tile of so few rows three waves would have none and one all the matrix products: the waves share the
+    // keys instead (512 tokens over 3000 and 48 single ones over 300 to 6000, 16 heads of 64: 593 us without, 340 with;
+    // 1 to 160 tokens over 200 to 1500: 33 and 28).  f16 tiles wait for memory either way (157 and 171).
+    if constexpr (DT == F32) {
+        if (n_rows <= FEW_ROWS) {
+            few_rows<DT, DP, FULL>(a, s, r0, kvh, sp, flat, reinterpret_cast<float*>(smem));
+            return;
+        }
+    }
 
     const int my = wave * 32 + m;
     const bool row = my < n_rows;
@@ -732,7 +767,7 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
         q[c] ^= flip;
     }
     const float abs_scale = fabsf(a.scale);
-    const float scale = RULES && a.cap > 0.0f ? abs_scale / a.cap : abs_scale * LOG2E;
+    const float scale = RULES && a.cap > 0.0f ? cap_rate(abs_scale, a.cap) : abs_scale * LOG2E;
     const float slope = RULES && a.slopes && row ? a.slopes[head] * LOG2E : 0.0f;
 
     const int* table = a.b.table + (int64_t)s * a.b.table_stride;
@@ -786,30 +821,51 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP <= 128 ? 2 : 1) void k_attn_m
     const int v_row = 4 * h + lane % 16 / 4, v_elem = 16 * (lane / 16 % 2) + 4 * (lane % 4);
     const int v_base = v_row * ROW + v_piece<DT, ROW>(v_row, v_elem / 8) * 16 + v_elem % 8 * 2;
 
-    const float unit = RULES ? 1.0f : scale;
+    // scores are kept in units of `unit` / log2 e: times scale, or as the tanh of a cap alone
+    const float unit = !RULES ? scale : a.cap > 0.0f && !a.slopes ? cap_unit(a.cap) : 1.0f;
     int page = 0, page_next = 0;
 
+    const bool in_range = DT == F16 && scale >= 1e-4f && scale <= 1e3f;
+    const float s2 = scale * scale, c1 = TANH_C[0] * scale, c3 = TANH_C[1] * scale * s2;
+    const float c5 = TANH_C[2] * scale * s2 * s2, c7 = TANH_C[3] * scale * s2 * s2 * s2;
+    const float c9 = TANH_C[4] * scale * s2 * s2 * s2 * s2;
     // cap and bias of the scores of tile j; score r of block k belongs to key j + 32 k + 8 (r / 4) + 4 h + r % 4
-    const float cap = a.cap * LOG2E, twice = 2.0f * LOG2E * scale;
     auto by_rule = [&](f16v (&sc)[KB], int j) INLINE {
         if (!RULES) return;
         if (a.cap > 0.0f) {
+            // A cap is there for the few scores that come near it: a wave whose tile has none past 3/4 of it forms six
+            // operations per score, the factor scale / cap in the coefficients (while these stay in range), and no
+            // transcendental one, which takes four times as long.  Mixed prompts, 112 row tiles of 8 key heads: 25.6 us,
+            // with the exponential form alone 27.4; 35 where every tile has scores past it (both forms for each score).
+            float most = 0.0f;
+            if (in_range) {
 #pragma unroll
-            for (int k = 0; k < KB; ++k)
+                for (int k = 0; k < KB; ++k)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    sc[k][r] = DT == F16 ? capped(sc[k][r], twice, cap) : cap * tanhf(sc[k][r] * scale);
+                    for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(sc[k][r]));
+            }
+            if (in_range && !__any(most * scale > TANH_SMALL)) {
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[k][r] = odd_poly(sc[k][r], c1, c3, c5, c7, c9);
+            } else {
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[k][r] = tanh_of<DT>(sc[k][r] * scale);
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < KB; ++k) sc[k] *= scale;
         }
         if (a.slopes) {
-            const float away = (float)(pos - j - 4 * h);
+            const float away = (float)(pos - j - 4 * h), first = a.cap > 0.0f ? cap_unit(a.cap) : 1.0f;
 #pragma unroll
             for (int k = 0; k < KB; ++k)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r]);
+                    sc[k][r] = fmaf(-slope, fabsf(away - (float)(32 * k + 8 * (r / 4) + r % 4)), sc[k][r] * first);
         }
     };
     // moves the reference when a score passes it by too much

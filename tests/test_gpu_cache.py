@@ -161,6 +161,34 @@ def test_attention_extreme_bounds(dtype, new):
             c.run(window=window, prefix=np.array(prefix), first=first)
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("scale,cap", [(0.125, 30.0), (0.125, 2.0), (-0.125, 3.0), (0.02, 0.04), (1e-7, 1.0), (0.125, 1e6),
+                                       (2e-6, 0.3), (0.0, 5.0), (50.0, 1.0)])
+def test_attention_caps(scale, cap, bias):
+    """Scores far under the cap, around half of it and past it, in one tile and apart; scales of any size."""
+    c = Case("f16", 4, 2, 64, 16, [1, 70, 40], [90, 300, 140], seed=16)
+    c.scale = scale
+    c.q[::3] *= 0.25
+    c.k[0][c.place(1, 100)] = 3.0
+    c.run(cap=cap, slopes=slopes(4) if bias else None)
+
+
+@pytest.mark.parametrize("hq,hk,d", [(2, 1, 64), (4, 4, 80), (1, 1, 256)])
+def test_attention_f32_tiles_of_few_rows(hq, hk, d):
+    """Sequences of one to sixteen rows beside long ones, and a long one's last rows, with each rule and masked junk."""
+    c = Case("f32", hq, hk, d, 16, [1, 130, 5, 0, 136, 8, 1], [700, 140, 5, 7, 500, 300, 33], seed=17)
+    c.table[0, 20] = -1
+    for s, j in ((0, 699), (1, 139), (4, 499)):
+        c.v[0][c.place(s, j)] = np.nan
+    first = np.array([max(0, p - 200) for _, _, p in R.positions(c.q_start, c.lens)])
+    last = np.array([i for i, (_, s, p) in enumerate(R.positions(c.q_start, c.lens)) if p == c.lens[s] - 1])
+    c.q[last] *= 2
+    with np.errstate(all="ignore"):
+        c.run(first=first)
+        c.run(window=40)
+        c.run(slopes=slopes(hq), cap=4.0)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("new", [1, 90])
 @pytest.mark.parametrize("d", [64, 80, 128, 256])
