@@ -132,7 +132,8 @@ __global__ __launch_bounds__(RT) void k_rope_append(RopeArgs a) {
     __shared__ float2 cs[PI_MAX_HEAD_DIM / 2];
     const int t = blockIdx.x;
     const int s = seq_of_row(a.b, t);
-    if (s >= a.b.n_seqs || a.b.q_start[s] > t) return;         // a row of no sequence
+    // a row of no sequence (s need not hold t: the first rows may not ascend, and pos has to stay under the length)
+    if (s >= a.b.n_seqs || a.b.q_start[s] > t || a.b.q_start[s + 1] <= t) return;
     // where the token lies in the cache (a length past the table is clamped as for reading)
     const int pos = clamped_len(a.b, a.c.page_shift, s) - (a.b.q_start[s + 1] - t);
     const int turn = a.positions ? a.positions[t] : pos;
