@@ -176,7 +176,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int s, int r0, int k
     const int d = FULL ? DP : a.c.head_dim;
     const int ps = a.c.page_size, shift = a.c.page_shift;
 
-    const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
+    int t0, t1;
+    seq_rows(a.b, s, t0, t1);
     const int len = clamped_len(a.b, shift, s), q_end = a.b.q_start[s + 1];
     const int n_rows = (int)min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)FEW_ROWS);
     if (n_rows <= 0) return;
@@ -590,8 +591,9 @@ __device__ __forceinline__ bool tile_at(const AttnArgs& a, int flat, int tile, i
     for (int base = 0; base < a.b.n_seqs; base += WAVE) {
         int n = 0;
         if (base + lane < a.b.n_seqs) {
-            const int t0 = max(a.b.q_start[base + lane], 0), t1 = min(a.b.q_start[base + lane + 1], a.b.n_tokens);
-            n = (int)((min(max((int64_t)t1 - t0, (int64_t)0) * a.group, most) + tile - 1) / tile);
+            int t0, t1;
+            seq_rows(a.b, base + lane, t0, t1);
+            n = (int)((min((int64_t)(t1 - t0) * a.group, most) + tile - 1) / tile);
         }
         const int incl = wave_incl_scan(n);
         const uint64_t past = __ballot(before + incl > flat);
@@ -694,7 +696,8 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1
     const int m = lane % 32, h = lane / 32;
     const int d = FULL ? DP : a.c.head_dim;
     const int ps = a.c.page_size, shift = a.c.page_shift;
-    const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
+    int t0, t1;
+    seq_rows(a.b, s, t0, t1);
     const int len = clamped_len(a.b, shift, s), q_end = a.b.q_start[s + 1];
     const int n_rows = (int)min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)MANY_ROWS);
 
@@ -1066,7 +1069,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     if (n <= 1) return;                           // written by the only one
     int s = flat, r0 = 0;
     if (a.rows > FEW_ROWS && !tile_at(a, flat, a.rows, a.most_rows, s, r0)) return;
-    const int t0 = max(a.b.q_start[s], 0), t1 = min(a.b.q_start[s + 1], a.b.n_tokens);
+    int t0, t1;
+    seq_rows(a.b, s, t0, t1);
     const int g = threadIdx.x / PIECES;
     const int i = blockIdx.x * PIECES + threadIdx.x % PIECES, r = i / pieces, e = (i - r * pieces) * 4;
     const bool row = r < min(min((int64_t)(t1 - t0) * a.group, a.most_rows) - r0, (int64_t)a.rows);

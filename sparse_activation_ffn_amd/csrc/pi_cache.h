@@ -101,6 +101,13 @@ __device__ __forceinline__ int clamped_len(const Batch& b, const int page_shift,
     return len < 0 ? 0 : len > cap ? (int)cap : len;
 }
 
+// rows t0 <= t < t1 of sequence s, inside the batch's rows whatever the first rows are; t1 - t0 is in 0..n_tokens (the
+// difference of two first rows as they are need not fit 32 bits)
+__device__ __forceinline__ void seq_rows(const Batch& b, int s, int& t0, int& t1) {
+    t0 = min(max(b.q_start[s], 0), b.n_tokens);
+    t1 = max(min(b.q_start[s + 1], b.n_tokens), t0);
+}
+
 // the sequence of row t: the number of sequences that end at or before t; found
 // by the whole wave (all 64 lanes call it with the same t).  n_seqs if none.
 __device__ __forceinline__ int seq_of_row(const Batch& b, int t) {
