@@ -68,6 +68,10 @@ __device__ __forceinline__ float weight_of(float m, float top) {
     return m == -INFINITY ? 0.0f : m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
 }
 
+// A partial sum in a join, times its weight f.  A weight of 0 takes finite sums out, but neither a NaN nor an infinity: a
+// NaN score leaves the reference as it is (-inf where a part has no other), so only the sums tell of it.
+__device__ __forceinline__ float part_of(float f, float v) { return f > 0.0f ? f * v : v - v == 0.0f ? 0.0f : v; }
+
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : (m - LIFT + __builtin_amdgcn_logf(l)) * LN2;
 }
@@ -492,9 +496,10 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int s, int r0, int k
 #pragma unroll
         for (int w = 0; w < FEW_WAVES; ++w) {
             const float f = weight_of(mw[w], all);
-            if (f == 0.0f) continue;
-            l += f * ml[(w * FEW_ROWS + r) * 2 + 1];
-            o += f * *reinterpret_cast<const f4*>(o_lds + (w * FEW_ROWS + r) * LD + e);
+            const f4 ow = *reinterpret_cast<const f4*>(o_lds + (w * FEW_ROWS + r) * LD + e);
+            l += part_of(f, ml[(w * FEW_ROWS + r) * 2 + 1]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[x] += part_of(f, ow[x]);
         }
         if (n_split > 1) {
             const int64_t at = (((int64_t)flat * a.c.kv_heads + kvh) * a.splits + sp) * a.rows + r;
@@ -1079,9 +1084,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     f4 o = f4{0, 0, 0, 0};
     auto add = [&](float2 ml, f4 v) INLINE {      // (a split that saw nothing holds no more than zeros)
         const float f = weight_of(ml.x, top);
-        if (f == 0.0f) return;
-        l += f * ml.y;
-        o += f * v;
+        l += part_of(f, ml.y);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] += part_of(f, v[x]);
     };
     if (row) {
 #pragma unroll 4
