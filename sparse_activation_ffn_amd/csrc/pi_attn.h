@@ -107,10 +107,11 @@ template <int DT>
 __device__ __forceinline__ void store_row(const AttnArgs& a, int t, int head, int e, f4 o, float m, float l) {
     typedef typename ElemT<DT>::T T;
     typedef typename ElemT<DT>::V4 V4;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const bool none = l == 0.0f;                  // (o may hold infinities and NaN of keys with scores of -inf)
+    const float inv = 1.0f / l;
     V4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (T)(o[i] * inv);
+    for (int i = 0; i < 4; ++i) v[i] = none ? (T)0.0f : (T)(o[i] * inv);
     *reinterpret_cast<V4*>((T*)a.out + t * a.o_ts + head * a.o_hs + e) = v;
     if (e == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + head] = lse_of(m, l);
 }

@@ -77,3 +77,16 @@ def test_values_that_weigh_nothing(dtype, hq, hk, new, lens, plant):
             for t, s, pos in R.positions(c.q_start, c.lens):
                 sees = pos >= int(at * (lens[s] - 1))
                 assert np.isfinite(got[t, :, 7]).all() != sees and np.isfinite(got[t, :, :7]).all(), (t, pos, at)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("hq,hk,new,lens", SHAPES)
+@pytest.mark.parametrize("plant", [1.0, np.nan, np.inf])
+def test_scores_of_minus_infinity_alone(dtype, hq, hk, new, lens, plant):
+    """A row whose scores are all -inf gets zeros and lse = -inf, whatever V holds."""
+    c = G.Case(dtype, hq, hk, 64, 16, new, lens, seed=24)
+    c.q[..., 0] = 1.0
+    c.k[..., 0] = -np.inf
+    c.v[:] = plant
+    got, lse = c.run(check=False)
+    assert (got == 0).all() and np.isneginf(lse).all()
