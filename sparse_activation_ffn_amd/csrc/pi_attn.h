@@ -94,8 +94,9 @@ __device__ __forceinline__ float tanh_of(float x) {
     return fabsf(x) <= TANH_SMALL ? odd_poly(x, TANH_C[0], TANH_C[1], TANH_C[2], TANH_C[3], TANH_C[4]) : big;
 }
 
-// scale / cap and cap log2 e, kept finite so that a product q.k of 0 stays 0
-__device__ __forceinline__ float cap_rate(float scale, float cap) { return fmaxf(-3e38f, fminf(scale / cap, 3e38f)); }
+// scale / cap, cap log2 e, scale log2 e and slope log2 e, kept finite so that a product q.k or a distance of 0 stays 0
+__device__ __forceinline__ float kept_finite(float f) { return f != f ? f : fmaxf(-3e38f, fminf(f, 3e38f)); }
+__device__ __forceinline__ float cap_rate(float scale, float cap) { return kept_finite(scale / cap); }
 __device__ __forceinline__ float cap_unit(float cap) { return fminf(cap, 2e38f) * LOG2E; }
 
 template <int DT> struct ElemT;
@@ -223,8 +224,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int s, int r0, int k
         q[c] = u4{0, 0, 0, 0};
         if (row && (FULL || e < d)) q[c] = ld16(a.q + (tok * a.q_ts + head * a.q_hs + e) * ES);
     }
-    const float slope = a.slopes && row ? a.slopes[head] * LOG2E : 0.0f;
-    const float scale = a.cap > 0.0f ? cap_rate(a.scale, a.cap) : a.scale * LOG2E;
+    const float slope = a.slopes && row ? kept_finite(a.slopes[head] * LOG2E) : 0.0f;
+    const float scale = a.cap > 0.0f ? cap_rate(a.scale, a.cap) : kept_finite(a.scale * LOG2E);
 
     const int* table = a.b.table + (int64_t)s * a.b.table_stride;
     const int last_page = (len - 1) >> shift;
@@ -776,8 +777,8 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1
         q[c] ^= flip;
     }
     const float abs_scale = fabsf(a.scale);
-    const float scale = RULES && a.cap > 0.0f ? cap_rate(abs_scale, a.cap) : abs_scale * LOG2E;
-    const float slope = RULES && a.slopes && row ? a.slopes[head] * LOG2E : 0.0f;
+    const float scale = RULES && a.cap > 0.0f ? cap_rate(abs_scale, a.cap) : kept_finite(abs_scale * LOG2E);
+    const float slope = RULES && a.slopes && row ? kept_finite(a.slopes[head] * LOG2E) : 0.0f;
 
     const int* table = a.b.table + (int64_t)s * a.b.table_stride;
     const int last_page = max(len - 1, 0) >> shift;

@@ -90,3 +90,22 @@ def test_scores_of_minus_infinity_alone(dtype, hq, hk, new, lens, plant):
     c.v[:] = plant
     got, lse = c.run(check=False)
     assert (got == 0).all() and np.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("hq,hk,new,lens", SHAPES)
+@pytest.mark.parametrize("scale", [3e38, -3e38, 1e-45])
+def test_scales_at_the_ends_of_32_bits(dtype, hq, hk, new, lens, scale):
+    """Scores of 0 stay 0: a plain mean."""
+    c = G.Case(dtype, hq, hk, 64, 16, new, lens, seed=25)
+    c.scale = scale
+    c.q[:] = 0
+    c.run()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("hq,hk,new,lens", SHAPES)
+def test_a_bias_at_the_end_of_32_bits(dtype, hq, hk, new, lens):
+    """A slope so steep that a row attends to its own key alone, whose distance is 0."""
+    c = G.Case(dtype, hq, hk, 64, 16, new, lens, seed=26)
+    c.run(slopes=np.full(hq, 3e38))
