@@ -9,7 +9,8 @@
 // passes it by more than SLACK (8), which is rare after the first keys.  The f16
 // weights for the matrix cores are carried 2^LIFT (64) times too large, so at
 // most 2^14, and small ones stay clear of f16's subnormals (they lose bits below
-// 2^-20 of the largest one).
+// 2^-20 of the largest one).  f32 weights are at most 2^8: values of any size up to
+// 2^120 divided by the number of keys are summed without overflow.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -27,7 +28,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float SLACK = 8.0f;
-constexpr float LIFT = 6.0f;
+template <int DT> constexpr float LIFT = DT == F16 ? 6.0f : 0.0f;
 constexpr int XCDS = 8;               // dies with an L2 each; workgroups go round them
 
 struct AttnArgs {
@@ -72,8 +73,9 @@ __device__ __forceinline__ float weight_of(float m, float top) {
 // NaN score leaves the reference as it is (-inf where a part has no other), so only the sums tell of it.
 __device__ __forceinline__ float part_of(float f, float v) { return f > 0.0f ? f * v : v - v == 0.0f ? 0.0f : v; }
 
+template <int DT>
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.0f ? -INFINITY : (m - LIFT + __builtin_amdgcn_logf(l)) * LN2;
+    return l == 0.0f ? -INFINITY : (m - LIFT<DT> + __builtin_amdgcn_logf(l)) * LN2;
 }
 
 // Capped scores are cap tanh(x), x = scale q.k / cap.  f32 caches: tanhf.  f16 caches: for |x| <= 3/4 x times a quartic in
@@ -114,7 +116,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int t, int head, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = none ? (T)0.0f : (T)(o[i] * inv);
     *reinterpret_cast<V4*>((T*)a.out + t * a.o_ts + head * a.o_hs + e) = v;
-    if (e == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + head] = lse_of(m, l);
+    if (e == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + head] = lse_of<DT>(m, l);
 }
 
 // ---- few rows: single tokens, and up to 16 rows per key head ------------------------
@@ -349,7 +351,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int s, int r0, int k
 #pragma unroll
                 for (int c = 0; c < VW; ++c) acc[n][c] *= f;
         }
-        const float off = LIFT - (ref == -INFINITY ? 0.0f : ref);
+        const float off = LIFT<DT> - (ref == -INFINITY ? 0.0f : ref);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -889,11 +891,21 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1
         if (__any(top > ref + SLACK)) {
             top = fmaxf(top, __shfl_xor(top, 32, WAVE));
             // (nothing is summed while ref is -inf but infinities, which no factor may turn into NaN)
-            const float now = fmaxf(ref, top), f = ref == -INFINITY ? 1.0f : fmaxf(weight_of(ref, now), 1e-37f);
+            const float now = fmaxf(ref, top), w = ref == -INFINITY ? 1.0f : weight_of(ref, now);
+            // of sums of f16 values a factor of 0 leaves 10^-37, which is less than 10^-18; f32 ones may be any size and
+            // become 0
+            const float f = fmaxf(w, 1e-37f);
             ref = now;
             sum *= f;
 #pragma unroll
-            for (int t = 0; t < ND; ++t) acc[t] *= f;
+            for (int t = 0; t < ND; ++t) {
+                if constexpr (DT == F16) {
+                    acc[t] *= f;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[t][i] = part_of(w, acc[t][i]);
+                }
+            }
         }
     };
     // one tile: its keys and values lie at cur, the next tile's go to next
@@ -974,7 +986,7 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1
             }
         }
         raise(sc);
-        const float off = LIFT - (ref == -INFINITY ? 0.0f : ref);
+        const float off = LIFT<DT> - (ref == -INFINITY ? 0.0f : ref);
         float part = 0.0f;
         if constexpr (DT == F16) {
             // V^T: elements 32 t + m of the keys 16 n + {4 h + i, 8 + 4 h + i} (rows 16 n + 4 h .. + 3, then 8

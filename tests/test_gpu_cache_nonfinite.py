@@ -109,3 +109,19 @@ def test_a_bias_at_the_end_of_32_bits(dtype, hq, hk, new, lens):
     """A slope so steep that a row attends to its own key alone, whose distance is 0."""
     c = G.Case(dtype, hq, hk, 64, 16, new, lens, seed=26)
     c.run(slopes=np.full(hq, 3e38))
+
+
+@pytest.mark.parametrize("hq,hk,new,lens", SHAPES)
+def test_large_values_at_keys_that_weigh_nothing(hq, hk, new, lens):
+    """f32 values of 10^36 at keys far below the last ones leave nothing in the output."""
+    c = G.Case("f32", hq, hk, 64, 16, new, lens, seed=27, sharp=0.1)
+    c.q[..., 0] = 60.0
+    c.k[..., 0] = 30.0
+    for s, n in enumerate(lens):
+        far = -(-n // 3)
+        for j in range(far):
+            p = c.place(s, j)
+            c.k[0, p[0], :, p[2], 0] = -30.0
+            if n > 3:
+                c.v[0, p[0], :, p[2]] *= 1e36
+    c.run()
