@@ -616,9 +616,9 @@ size_t pi_pages_workspace_bytes(const pi_page_state* state, int32_t n);
  * gets the copy.  In list order, a sequence is granted its pages as long as
  * the sum of the needs up to and including it is at most the number of free
  * pages, and it takes the lowest free ones, first the copy, then the new
- * ones; its length grows by add[i].  One that would pass table_stride pages
- * needs nothing and is not granted, like one with add[i] < 0 or an id outside
- * the table.
+ * ones; its length grows by add[i].  One that would pass table_stride pages or
+ * 2^30 tokens needs nothing and is not granted, like one with add[i] < 0 or an
+ * id outside the table.
  *   granted [n] int32, out: 1 or 0.
  *   copies [2][n] int32, out: the copied page and its copy, or -1, -1.
  *   cache: its pages are copied in every layer (cache->pages == state->pages,

@@ -94,9 +94,14 @@ inline pi_status check_rows(const pi_rows* r, const char* name, int dtype) {
 
 // ---- device ---------------------------------------------------------------------
 
-// tokens of sequence s that its table can hold (and 2^30 at most: sums of two stay in 32 bits)
+// tokens that a table row can hold, and 2^30 at most: sums of two lengths stay in 32 bits
+__device__ __forceinline__ int64_t longest(int table_stride, int page_shift) {
+    return min((int64_t)table_stride << page_shift, (int64_t)1 << 30);
+}
+
+// the length of sequence s, inside what its table can hold
 __device__ __forceinline__ int clamped_len(const Batch& b, const int page_shift, int s) {
-    const int64_t cap = min((int64_t)b.table_stride << page_shift, (int64_t)1 << 30);
+    const int64_t cap = longest(b.table_stride, page_shift);
     const int len = b.kv_len[s];
     return len < 0 ? 0 : len > cap ? (int)cap : len;
 }

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(PT) void k_pages_extend(pi_page_state st, const int
         if (i < n) {
             const int s = seqs[i], a = add[i];
             if (s >= 0 && s < st.max_seqs && a >= 0) {
-                const int64_t len = st.lens[s], cap = (int64_t)st.table_stride << shift;
+                const int64_t len = st.lens[s], cap = longest(st.table_stride, shift);
                 if (len >= 0 && len + a <= cap) {
                     fits = true;
                     const int have = (int)((len + st.page_size - 1) >> shift);
