@@ -102,7 +102,7 @@ class AttentionLayer:
 
 class DecoderLayer:
     """Attention and the predictor-gated sparse FFN, each after a norm and added to its input:
-    x += attention(norm(x)); x += ffn(norm(x)).  x [tokens][d] in f16."""
+    x += attention(norm(x)); x += ffn(norm(x)).  x [tokens][d] in the cache's dtype."""
 
     def __init__(self, attention: AttentionLayer, ffn: DeviceLayer, eps: float = 1e-5):
         self.attention, self.ffn, self.eps = attention, ffn, eps
@@ -120,7 +120,7 @@ class DecoderLayer:
             if n not in self.buffers:
                 self.buffers[n] = StepBuffers(self.ffn, n, x.device)
             y = decode_step(self.ffn, part.contiguous(), self.buffers[n], self.predictor, self.parts)
-            out.append(y.to(x.dtype))
+            out.append(y.to(x.dtype, copy=True))      # (the buffers are the next run's)
         return torch.cat(out)
 
     def __call__(self, x: torch.Tensor, cache: PagedCache, layer: int, batch: pb.SeqBatch):
