@@ -87,6 +87,7 @@ def main():
     cache.compact()
     used = int((cache.refs > 0).sum())
     t = time.perf_counter() - t
+    assert int(cache.lens[0]) == longest, "the pool ran out of pages"
     assert used == -(-longest // 16) and bool((cache.refs[:used] == 1).all()) and bool(x.isfinite().all())
     print(f"prompt of {a.prompt}, {a.beams} beams of {a.steps} steps through {a.layers} layers in {1e3 * t:.1f} ms; "
           f"{used} of {pages} pages in use, the first {used}")

@@ -619,7 +619,10 @@ size_t pi_pages_workspace_bytes(const pi_page_state* state, int32_t n);
  * ones; its length grows by add[i].  One that would pass table_stride pages or
  * 2^30 tokens needs nothing and is not granted, like one with add[i] < 0 or an
  * id outside the table.
- *   granted [n] int32, out: 1 or 0.
+ *   granted [n] int32, out: 1 or 0.  A sequence that was not granted keeps its
+ *          length and may still share its last page: a batch that gives it new
+ *          tokens would write them over its last ones.  Its length in the batch
+ *          must be 0 then (nothing is written, its rows see nothing).
  *   copies [2][n] int32, out: the copied page and its copy, or -1, -1.
  *   cache: its pages are copied in every layer (cache->pages == state->pages,
  *          same page_size); NULL: the caller copies (pi_pages_copy).

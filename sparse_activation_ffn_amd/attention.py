@@ -36,17 +36,25 @@ class PagedCache:
         self.ws = torch.empty(pb.pi_pages_workspace_bytes(self.state, max_seqs),
                               dtype=torch.uint8, device=device)
         self.moved = torch.empty(pages, **i32)
+        # whether a sequence's last extension was granted; one more place, 0, for ids outside the table
+        self.room = torch.ones(max_seqs + 1, **i32)
+        self.room[max_seqs] = 0
 
     def ids(self, seqs: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(seqs), dtype=torch.int32, device=self.device)
 
+    def _slots(self, seqs: torch.Tensor) -> torch.Tensor:
+        return torch.where((seqs >= 0) & (seqs < self.max_seqs), seqs, self.max_seqs).long()
+
     def extend(self, seqs: torch.Tensor, add: torch.Tensor):
         """Room for add[i] more tokens in sequence seqs[i] (int32 device tensors); a shared last
-        page is copied first.  Returns (granted [n], copies [2][n]) on the device."""
+        page is copied first.  Returns (granted [n], copies [2][n]) on the device.  A sequence that
+        is not granted has no part in the batches until an extension of it is."""
         n = seqs.numel()
         granted = torch.empty(n, dtype=torch.int32, device=self.device)
         copies = torch.empty((2, n), dtype=torch.int32, device=self.device)
         pb.pi_pages_extend(self.state, self.cache, seqs, add, granted, copies, self.ws)
+        self.room.scatter_(0, self._slots(seqs), granted)
         return granted, copies
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor):
@@ -63,12 +71,17 @@ class PagedCache:
 
     def batch(self, seqs: torch.Tensor, new: Sequence[int], max_len: int) -> pb.SeqBatch:
         """The batch of these sequences (after extend), new[i] new tokens each: rows of the step's
-        tensors in this order.  max_len bounds their lengths (the host's own count of tokens)."""
+        tensors in this order.  max_len bounds their lengths (the host's own count of tokens).  A
+        sequence whose extension was not granted has no place for its new tokens: it goes in with
+        length 0, so nothing is written for it (its last places may be shared, and hold other
+        tokens) and its rows see nothing."""
         starts = [0]
         for n in new:
             starts.append(starts[-1] + n)
-        at = seqs.long()
-        return pb.make_seq_batch(self.ids(starts), self.lens[at], self.table[at], starts[-1],
+        slot = self._slots(seqs)
+        at = slot.clamp_max(self.max_seqs - 1)
+        lens = torch.where(self.room[slot] > 0, self.lens[at], 0)
+        return pb.make_seq_batch(self.ids(starts), lens, self.table[at], starts[-1],
                                  max(list(new) + [0]), max_len)
 
 

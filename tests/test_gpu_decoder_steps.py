@@ -45,3 +45,58 @@ def test_a_result_is_the_callers():
     kept = a.clone()
     layer.feed_forward(torch.randn((5, D), device=DEV))
     assert torch.equal(a, kept)
+
+
+def test_a_sequence_without_pages_leaves_the_others_alone():
+    """A pool that runs dry under four beams with a shared last page: two get their pages, the others write nothing
+    and see nothing until there is room again, and every token that was in the cache keeps its bits."""
+    layer = decoder_layer().attention
+    x = torch.randn((24, D), device=DEV).half()
+    y = torch.randn((4, D), device=DEV).half()
+    outs = []
+    for pages in (40, 4):                                            # 24 tokens: one full page and a shared half one
+        cache = PagedCache(1, pages, HK, HD, 4, 64)
+        first, all4, one = cache.ids([0]), cache.ids([0, 1, 2, 3]), cache.ids([1] * 4)
+        cache.extend(first, cache.ids([24]))
+        layer(x, cache, 0, cache.batch(first, [24], 24))
+        cache.fork(cache.ids([0] * 3), cache.ids([1, 2, 3]))
+        k, v = cache.k.clone(), cache.v.clone()
+        granted, copies = cache.extend(all4, one)
+        out = layer(y, cache, 0, cache.batch(all4, [1] * 4, 25))
+        outs.append(out)
+        if pages == 40:
+            assert granted.tolist() == [1] * 4
+            continue
+        assert granted.tolist() == [1, 1, 0, 0] and cache.lens.tolist() == [25, 25, 24, 24]
+        assert torch.equal(out[:2], outs[0][:2]) and bool((out[2:] == 0).all())
+        # the old pages are as they were; the copies differ from theirs at the new token alone
+        old, made = copies[0, :2].long(), copies[1, :2].long()
+        for now, was in ((cache.k, k), (cache.v, v)):
+            same = [p for p in range(4) if p not in made.tolist()]
+            assert torch.equal(now[:, same], was[:, same])
+            assert torch.equal(now[:, made, :, :8], was[:, old, :, :8])
+            assert torch.equal(now[:, made, :, 9:], was[:, old, :, 9:])
+        # refused again, then granted once a beam has gone: as in the roomy pool
+        granted, _ = cache.extend(cache.ids([2]), cache.ids([40]))
+        again = layer(y[2:3], cache, 0, cache.batch(cache.ids([2]), [1], 25))
+        assert granted.tolist() == [0] and bool((again == 0).all())
+        cache.free(cache.ids([0]))
+        granted, _ = cache.extend(cache.ids([2]), cache.ids([1]))
+        again = layer(y[2:3], cache, 0, cache.batch(cache.ids([2]), [1], 25))
+        assert granted.tolist() == [1] and (again - outs[0][2:3]).abs().max() < 8 * 2.0 ** -11
+
+
+def test_ids_outside_the_table_take_no_part():
+    layer = decoder_layer().attention
+    cache = PagedCache(1, 10, HK, HD, 4, 64)
+    x = torch.randn((5, D), device=DEV).half()
+    cache.extend(cache.ids([0, 1]), cache.ids([5, 5]))
+    layer(torch.cat([x, x]), cache, 0, cache.batch(cache.ids([0, 1]), [5, 5], 5))
+    k = cache.k.clone()
+    ids = cache.ids([-1, 4, 2 ** 31 - 1, 1])
+    granted, _ = cache.extend(ids, cache.ids([1] * 4))
+    out = layer(x[:4], cache, 0, cache.batch(ids, [1] * 4, 6))
+    assert granted.tolist() == [0, 0, 0, 1] and cache.lens.tolist() == [5, 6, 0, 0]
+    assert bool((out[:3] == 0).all()) and bool((out[3] != 0).any())
+    changed = (cache.k != k).any(-1).any(2)[0]                        # [page][place]
+    assert changed.nonzero().tolist() == [[int(cache.table[1, 0]), 5]]
