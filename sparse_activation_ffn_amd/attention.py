@@ -41,7 +41,8 @@ class PagedCache:
         self.room[max_seqs] = 0
 
     def ids(self, seqs: Sequence[int]) -> torch.Tensor:
-        return torch.tensor(list(seqs), dtype=torch.int32, device=self.device)
+        # from pinned memory, so that the copy is enqueued and not waited for
+        return torch.tensor(list(seqs), dtype=torch.int32, pin_memory=True).to(self.device, non_blocking=True)
 
     def _slots(self, seqs: torch.Tensor) -> torch.Tensor:
         return torch.where((seqs >= 0) & (seqs < self.max_seqs), seqs, self.max_seqs).long()

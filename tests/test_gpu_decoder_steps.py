@@ -100,3 +100,50 @@ def test_ids_outside_the_table_take_no_part():
     assert bool((out[:3] == 0).all()) and bool((out[3] != 0).any())
     changed = (cache.k != k).any(-1).any(2)[0]                        # [page][place]
     assert changed.nonzero().tolist() == [[int(cache.table[1, 0]), 5]]
+
+
+def test_steps_do_not_wait():
+    """A step's bookkeeping and layers only enqueue: the host is through while the stream is still at work before them."""
+    layer = decoder_layer()
+    cache = PagedCache(1, 40, HK, HD, 4, 100)
+    x = torch.randn((4, D), device=DEV).half()
+
+    def step(length):
+        everyone = cache.ids(range(4))
+        cache.fork(cache.ids([0, 0, 1, 1]), everyone)
+        cache.extend(everyone, cache.ids([1] * 4))
+        return layer(x, cache, 0, cache.batch(everyone, [1] * 4, length))
+    for n in range(1, 4):                                            # buffers, workspaces and pinned blocks are there
+        step(n)
+    torch.cuda.synchronize()
+    a = torch.randn((8192, 8192), device=DEV)
+    done = torch.cuda.Event()
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        for _ in range(20):                                          # 100 ms and more
+            a = (a @ a).clamp_(-1, 1)
+        step(4)
+        step(5)
+        done.record()
+        assert not done.query()
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    torch.cuda.synchronize()
+    assert cache.lens.tolist() == [5] * 4
+
+
+def test_the_example_decodes_without_a_wait():
+    spec = importlib.util.spec_from_file_location("beam_decode", os.path.join(ROOT, "examples", "beam_decode.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layers = [decoder_layer(seed=i) for i in range(2)]
+    prompt = torch.randn((75, D), device=DEV).half()
+    outs = []
+    for mode in ("default", "error"):
+        cache = PagedCache(2, 60, HK, HD, 4, 100)
+        torch.cuda.set_sync_debug_mode(mode)
+        try:
+            outs.append(example.decode(layers, cache, prompt, 4, 7, chunk=32))
+        finally:
+            torch.cuda.set_sync_debug_mode("default")
+    assert torch.equal(outs[0], outs[1])
