@@ -120,7 +120,7 @@ class DecoderLayer:
 
     def __init__(self, attention: AttentionLayer, ffn: DeviceLayer, eps: float = 1e-5):
         self.attention, self.ffn, self.eps = attention, ffn, eps
-        self.parts, self.predictor, self.buffers = ffn.parts(), ffn.predictor(), {}
+        self.buffers = {}
 
     def norm(self, x: torch.Tensor) -> torch.Tensor:
         return torch.nn.functional.layer_norm(x.float(), x.shape[-1:], eps=self.eps).to(x.dtype)
@@ -128,12 +128,14 @@ class DecoderLayer:
     def feed_forward(self, x: torch.Tensor) -> torch.Tensor:
         """The sparse FFN, in runs of at most PI_MAX_BATCH tokens (a call's union of active
         neurons grows with its tokens)."""
+        # as the FFN is now: a new index, a placement or a threshold replaces what the descriptors name
+        parts, predictor = self.ffn.parts(), self.ffn.predictor()
         out = []
         for part in x.split(pb.PI_MAX_BATCH):
             n = part.shape[0]
-            if n not in self.buffers:
+            if n not in self.buffers or self.buffers[n].lists.n_hot != self.ffn.n_hot:
                 self.buffers[n] = StepBuffers(self.ffn, n, x.device)
-            y = decode_step(self.ffn, part.contiguous(), self.buffers[n], self.predictor, self.parts)
+            y = decode_step(self.ffn, part.contiguous(), self.buffers[n], predictor, parts)
             out.append(y.to(x.dtype, copy=True))      # (the buffers are the next run's)
         return torch.cat(out)
 

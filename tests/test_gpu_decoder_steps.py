@@ -147,3 +147,32 @@ def test_the_example_decodes_without_a_wait():
         finally:
             torch.cuda.set_sync_debug_mode("default")
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_the_ffn_may_be_maintained_between_steps(dtype):
+    """After a new index, a placement on the host or a new threshold the layer runs on what its FFN holds now, for
+    token counts that it has met and for others: the same bits as a layer made of the FFN as it is."""
+    layer = decoder_layer(dtype, n_hot=300)
+    x = torch.randn((70, D), device=DEV).to(dtype)
+
+    def same():
+        fresh = DecoderLayer(layer.attention, layer.ffn)
+        for n in (1, 3, 5, 70):
+            assert torch.equal(layer.feed_forward(x[:n]), fresh.feed_forward(x[:n])), n
+    for n in (1, 3):
+        layer.feed_forward(x[:n])
+    counts = torch.randint(0, 1000, (layer.ffn.n,), dtype=torch.int32, device=DEV)
+    before = layer.feed_forward(x[:3])
+    layer.ffn.reindex(counts, 700, 1)                                # 700 hot rows from now on
+    assert layer.ffn.n_hot == 700
+    same()
+    assert (layer.feed_forward(x[:3]).float() - before.float()).abs().max() < 2.0 ** -9 * before.abs().max()
+    layer.ffn.place_cold_on_host()
+    host = layer.ffn.cold_host["W_up"]
+    host.zero_()                                                     # the rows that a step reads from now on
+    torch.cuda.synchronize()
+    same()
+    layer.ffn.threshold = 1e9                                        # no neuron is active
+    assert bool((layer.feed_forward(x[:3]) == 0).all())
+    same()
