@@ -111,7 +111,7 @@ class AttentionLayer:
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.empty(need, dtype=torch.uint8, device=x.device)
         pb.pi_paged_attention(cache.cache, layer, batch, self.rule, q, q, None, self.ws)
-        return q.reshape(x.shape[0], -1) @ self.w_o.t()
+        return q.reshape(x.shape[0], self.q_heads * self.head_dim) @ self.w_o.t()
 
 
 class DecoderLayer:
@@ -128,6 +128,8 @@ class DecoderLayer:
     def feed_forward(self, x: torch.Tensor) -> torch.Tensor:
         """The sparse FFN, in runs of at most PI_MAX_BATCH tokens (a call's union of active
         neurons grows with its tokens)."""
+        if x.shape[0] == 0:
+            return torch.empty_like(x)
         # as the FFN is now: a new index, a placement or a threshold replaces what the descriptors name
         parts, predictor = self.ffn.parts(), self.ffn.predictor()
         out = []

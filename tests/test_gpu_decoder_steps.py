@@ -176,3 +176,21 @@ def test_the_ffn_may_be_maintained_between_steps(dtype):
     layer.ffn.threshold = 1e9                                        # no neuron is active
     assert bool((layer.feed_forward(x[:3]) == 0).all())
     same()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_steps_without_tokens(dtype):
+    """No rows at all, and sequences without new tokens among others."""
+    layer = decoder_layer(dtype)
+    cache = PagedCache(1, 10, HK, HD, 3, 64, dtype=dtype)
+    x = torch.randn((4, D), device=DEV).to(dtype)
+    none = layer(x[:0], cache, 0, cache.batch(cache.ids([]), [], 0))
+    assert none.shape == (0, D) and none.dtype == dtype
+    ids = cache.ids([0, 1, 2])
+    cache.extend(ids, cache.ids([0, 4, 0]))
+    none = layer(x[:0], cache, 0, cache.batch(ids, [0, 0, 0], 4))
+    assert none.shape == (0, D)
+    out = layer(x, cache, 0, cache.batch(ids, [0, 4, 0], 4))
+    alone = PagedCache(1, 10, HK, HD, 1, 64, dtype=dtype)
+    alone.extend(alone.ids([0]), alone.ids([4]))
+    assert torch.equal(out, layer(x, alone, 0, alone.batch(alone.ids([0]), [4], 4)))
