@@ -378,6 +378,7 @@ def pi_rope_append(cache: KvCache, layer: int, batch: SeqBatch, rope: Rope, q, q
     [tokens][kv_heads][head_dim]; the elements of a head contiguous, other strides free."""
     hq = 0 if q is None else q.shape[1]
     hk, dt, d, n = cache.kv_heads, cache.dtype, cache.head_dim, batch.n_tokens
+    _vector("positions", positions, "int32", n)
     _check(lib().pi_rope_append(
         C.byref(cache), layer, C.byref(batch), C.byref(rope), ptr(positions), hq,
         None if q is None else _rows(q, dt, d, n, hq),
@@ -393,6 +394,10 @@ def pi_paged_attention(cache: KvCache, layer: int, batch: SeqBatch, rule: ScoreR
                        lse=None, ws=None, stream=None):
     """q and out [tokens][q_heads][head_dim], lse [tokens][q_heads] float32 or None."""
     hq, dt, d, n = q.shape[1], cache.dtype, cache.head_dim, batch.n_tokens
+    _vector("lse", lse, "float32", n * hq)
+    for (name, have), need in zip(getattr(rule, "_sizes", ()), (hq, batch.n_seqs, n)):
+        if have is not None and have < need:
+            raise ValueError(f"{name} must have at least {need} elements, has {have}")
     _check(lib().pi_paged_attention(
         C.byref(cache), layer, C.byref(batch), C.byref(rule), hq, _rows(q, dt, d, n, hq),
         _rows(out, dt, d, n, hq), ptr(lse), ptr(ws),
@@ -406,27 +411,36 @@ def pi_pages_workspace_bytes(state: PageState, n: int) -> int:
 def pi_pages_extend(state: PageState, cache: Optional[KvCache], seqs, add, granted, copies, ws,
                     stream=None):
     """seqs, add, granted: int32 [n]; copies: int32 [2][n]."""
+    n = seqs.numel()
+    for name, t, size in (("seqs", seqs, n), ("add", add, n), ("granted", granted, n), ("copies", copies, 2 * n)):
+        _vector(name, t, "int32", size)
     _check(lib().pi_pages_extend(C.byref(state), None if cache is None else C.byref(cache),
-                                 ptr(seqs), ptr(add), seqs.numel(), ptr(granted), ptr(copies),
+                                 ptr(seqs), ptr(add), n, ptr(granted), ptr(copies),
                                  ptr(ws), ws.numel() * ws.element_size(), stream_handle(stream)))
 
 
 def pi_pages_fork(state: PageState, src, dst, ws, stream=None):
+    _vector("src", src, "int32", 0)
+    _vector("dst", dst, "int32", src.numel())
     _check(lib().pi_pages_fork(C.byref(state), ptr(src), ptr(dst), src.numel(), ptr(ws),
                                ws.numel() * ws.element_size(), stream_handle(stream)))
 
 
 def pi_pages_free(state: PageState, seqs, stream=None):
+    _vector("seqs", seqs, "int32", 0)
     _check(lib().pi_pages_free(C.byref(state), ptr(seqs), seqs.numel(), stream_handle(stream)))
 
 
 def pi_pages_compact(state: PageState, cache: Optional[KvCache], moved, ws, stream=None):
+    _vector("moved", moved, "int32", state.pages)
     _check(lib().pi_pages_compact(C.byref(state), None if cache is None else C.byref(cache),
                                   ptr(moved), ptr(ws), ws.numel() * ws.element_size(),
                                   stream_handle(stream)))
 
 
 def pi_pages_copy(cache: KvCache, src, dst, stream=None):
+    _vector("src", src, "int32", 0)
+    _vector("dst", dst, "int32", src.numel())
     _check(lib().pi_pages_copy(C.byref(cache), ptr(src), ptr(dst), src.numel(),
                                stream_handle(stream)))
 
@@ -496,13 +510,20 @@ def make_seq_batch(q_start, kv_len, table, n_tokens: int, max_new: int, max_len:
 def make_score_rule(scale: float, cap: float = 0.0, slopes=None, window: int = 0, prefix=None,
                     first=None) -> ScoreRule:
     """slopes float32 [q_heads], prefix int32 [n_seqs], first int32 [n_tokens] (device) or None."""
+    _vector("slopes", slopes, "float32", 0)
+    _vector("prefix", prefix, "int32", 0)
+    _vector("first", first, "int32", 0)
     r = ScoreRule(float(scale), float(cap), int(window), ptr(slopes), ptr(prefix), ptr(first))
     r._keep = (slopes, prefix, first)
+    # how many there are is compared where the batch is known
+    r._sizes = [(name, t.numel() if hasattr(t, "numel") else None)
+                for name, t in (("slopes", slopes), ("prefix", prefix), ("first", first))]
     return r
 
 
 def make_rope(turns, pairs: bool = False, magnitude: float = 1.0) -> Rope:
     """turns: float64 device tensor [rotary_dim / 2] (pi_rope_turns)."""
+    _vector("turns", turns, "float64", 0)
     r = Rope(2 * turns.numel(), PI_ROPE_PAIRS if pairs else PI_ROPE_HALVES, ptr(turns) or None,
              float(magnitude))
     r._keep = turns
@@ -523,6 +544,21 @@ def make_page_state(refs, table, lens, page_size: int) -> PageState:
 def _int32(name: str, t, shape):
     if str(t.dtype) != "torch.int32" or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+_torch_dtypes: dict = {}
+
+
+def _vector(name: str, t, dtype: str, n: int):
+    """Refuses a tensor (None and addresses pass) that does not hold n elements of dtype one after the other."""
+    if t is None or isinstance(t, int):
+        return
+    if not _torch_dtypes:
+        import torch
+        _torch_dtypes.update(int32=torch.int32, float32=torch.float32, float64=torch.float64)
+    if t.dtype is not _torch_dtypes[dtype] or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements, "
+                         f"got {tuple(t.shape)} of {t.dtype}")
 
 
 def _rows(t, dtype: int, head_dim: int, n_tokens: int, heads: int):
