@@ -553,12 +553,14 @@ def _vector(name: str, t, dtype: str, n: int):
     """Refuses a tensor (None and addresses pass) that does not hold n elements of dtype one after the other."""
     if t is None or isinstance(t, int):
         return
+    if t.dtype is _torch_dtypes.get(dtype) and t.numel() >= n and t.is_contiguous():
+        return
     if not _torch_dtypes:
         import torch
         _torch_dtypes.update(int32=torch.int32, float32=torch.float32, float64=torch.float64)
-    if t.dtype is not _torch_dtypes[dtype] or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements, "
-                         f"got {tuple(t.shape)} of {t.dtype}")
+        return _vector(name, t, dtype, n)
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements, "
+                     f"got {tuple(t.shape)} of {t.dtype}")
 
 
 def _rows(t, dtype: int, head_dim: int, n_tokens: int, heads: int):

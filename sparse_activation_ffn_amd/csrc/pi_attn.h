@@ -69,9 +69,12 @@ __device__ __forceinline__ float weight_of(float m, float top) {
     return m == -INFINITY ? 0.0f : m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
 }
 
-// A partial sum in a join, times its weight f.  A weight of 0 takes finite sums out, but neither a NaN nor an infinity: a
-// NaN score leaves the reference as it is (-inf where a part has no other), so only the sums tell of it.
-__device__ __forceinline__ float part_of(float f, float v) { return f > 0.0f ? f * v : v - v == 0.0f ? 0.0f : v; }
+// Adds a part (sum of weights pl, sums of values po) times its weight f.  A weight of 0 is multiplied too: a NaN score leaves
+// the reference as it is (-inf where a part has no other), so only the sums tell of it.
+__device__ __forceinline__ void add_part(float f, float pl, f4 po, float& l, f4& o) {
+    l += f * pl;
+    o += f * po;
+}
 
 template <int DT>
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -500,10 +503,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int s, int r0, int k
 #pragma unroll
         for (int w = 0; w < FEW_WAVES; ++w) {
             const float f = weight_of(mw[w], all);
-            const f4 ow = *reinterpret_cast<const f4*>(o_lds + (w * FEW_ROWS + r) * LD + e);
-            l += part_of(f, ml[(w * FEW_ROWS + r) * 2 + 1]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] += part_of(f, ow[x]);
+            add_part(f, ml[(w * FEW_ROWS + r) * 2 + 1], *reinterpret_cast<const f4*>(o_lds + (w * FEW_ROWS + r) * LD + e), l, o);
         }
         if (n_split > 1) {
             const int64_t at = (((int64_t)flat * a.c.kv_heads + kvh) * a.splits + sp) * a.rows + r;
@@ -897,14 +897,14 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1
             const float f = fmaxf(w, 1e-37f);
             ref = now;
             sum *= f;
+            if (DT == F16 || !__any(w < f)) {
 #pragma unroll
-            for (int t = 0; t < ND; ++t) {
-                if constexpr (DT == F16) {
-                    acc[t] *= f;
-                } else {
+                for (int t = 0; t < ND; ++t) acc[t] *= f;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[t][i] = part_of(w, acc[t][i]);
-                }
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[t][i] = w > 0.0f ? w * acc[t][i] : finite(acc[t][i]) ? 0.0f : acc[t][i];
             }
         }
     };
@@ -1096,12 +1096,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     const int64_t at = ((int64_t)flat * a.c.kv_heads + kvh) * a.splits * a.rows + r;
     float top = -INFINITY, l = 0.0f;
     f4 o = f4{0, 0, 0, 0};
-    auto add = [&](float2 ml, f4 v) INLINE {      // (a split that saw nothing holds no more than zeros)
-        const float f = weight_of(ml.x, top);
-        l += part_of(f, ml.y);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[x] += part_of(f, v[x]);
-    };
+    // (a split that saw nothing holds no more than zeros)
+    auto add = [&](float2 ml, f4 v) INLINE { add_part(weight_of(ml.x, top), ml.y, v, l, o); };
     if (row) {
 #pragma unroll 4
         for (int k = g; k < n; k += GROUPS) top = fmaxf(top, a.part_ml[at + (int64_t)k * a.rows].x);
