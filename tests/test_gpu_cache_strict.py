@@ -54,3 +54,25 @@ def test_rope_append_many_sequences(n):
     for t, s, pos in R.positions(c.q_start, c.lens):
         want[c.place(s, pos)] = x[t]
     assert np.array_equal(v[0].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("hq,hk,d,new,lens", [(8, 1, 128, [1, 1], [9001, 700]), (2, 2, 64, [1], [20000]), (4, 2, 80, [6], [7000]),
+                                              (2, 1, 64, [100, 1], [5000, 3000]), (2, 1, 256, [70], [3000])])
+def test_attention_masked_values_in_splits(dtype, hq, hk, d, new, lens):
+    """Junk that no row sees, in pieces of the keys where some rows see nothing at all, stays out of the joins."""
+    c = G.Case(dtype, hq, hk, d, 16, new, lens, seed=30)
+    c.k[:, c.free], c.v[:, c.free] = np.nan, np.inf
+    for s, n in enumerate(lens):
+        used = n % 16
+        if used:
+            c.k[0, c.table[s, (n - 1) // 16], :, used:], c.v[0, c.table[s, (n - 1) // 16], :, used:] = np.nan, -np.inf
+        for j in range(1000 if n > 2000 else 200):                    # before the first key of every row
+            p = c.place(s, j)
+            c.k[0][p], c.v[0][p] = np.inf, np.nan
+    rows = list(R.positions(c.q_start, c.lens))
+    lowest = np.array([1000 if lens[s] > 2000 else 200 for _, s, _ in rows])
+    c.run(first=lowest)
+    # every second row sees its last keys alone, the rows between them everything from the lowest on
+    c.run(first=np.where(np.arange(c.T) % 2 == 0, np.array([p for _, _, p in rows]) - 2, lowest))
+    c.run(first=lowest, window=300)
