@@ -341,7 +341,8 @@ __global__ __launch_bounds__(PT) void k_pages_extend(pi_page_state st, const int
         int* row = st.table + (int64_t)s * st.table_stride;
         auto take = [&](int* row, int begin, int from, int e) {
             const int p = free_ids[from + e];
-            if (begin + e < st.table_stride) row[begin + e] = p;
+            // (a sequence named twice may have any length by now)
+            if ((unsigned)(begin + e) < (unsigned)st.table_stride) row[begin + e] = p;
             st.refs[p] = 1;
         };
         if (ok && need <= FEW)
