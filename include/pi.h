@@ -576,9 +576,15 @@ typedef struct pi_score_rule {
  * Keys that a row does not see have no influence on it, whatever they hold
  * (infinities and NaN included).  Scores, weights, sums and outputs are float32
  * until the output is rounded once; with PI_F16 the weights are rounded to f16
- * for the product with V (relative error 2^-12 each), their sum is not.  out may
- * be q.
- * Needs a workspace of pi_attention_workspace_bytes (256-byte aligned).
+ * for the product with V (an error of 2^-11 of each, or of 2^-31 of the row's
+ * largest where that is more), their sum is not.  With PI_F32 the sums overflow
+ * where 2^8 times the sum of |V| over the keys that a row sees passes 2^128.  A
+ * NaN score, or a NaN or an infinity in V at a key with a score above -inf, that
+ * a row sees reaches its output.  out may be q.
+ * Needs a workspace of pi_attention_workspace_bytes (256-byte aligned).  A call
+ * is refused (PI_ERR_SHAPE) past 2^23 workgroups: n_seqs * kv_heads times the
+ * splits of the keys, for more than 16 rows per key head row tiles of 128
+ * instead of sequences.
  */
 size_t pi_attention_workspace_bytes(const pi_kv_cache* cache, const pi_seq_batch* batch,
                                     int32_t q_heads);

@@ -82,7 +82,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // Capped scores are cap tanh(x), x = scale q.k / cap.  f32 caches: tanhf.  f16 caches: for |x| <= 3/4 x times a quartic in
-// x^2 (its coefficients are those of the least largest relative error, 6e-7, found by weighted least squares), else
+// x^2 (its coefficients are those of the least largest relative error, 6.1e-7, found by weighted least squares; 7.0e-7 with
+// the roundings of f32), else
 // 1 - 2 / (e^2x + 1), which is within 2^-22 and so within 1e-6 of the value there, but not for small x.
 constexpr float TANH_SMALL = 0.75f;
 
@@ -688,7 +689,7 @@ __global__ __launch_bounds__(WAVE * MANY_WAVES, DP == 64 ? 3 : DP == 128 ? 2 : 1
     constexpr int LOADS = TILE / RPI / MANY_WAVES; // load instructions per wave, K and V each
     extern __shared__ __align__(1024) uint8_t smem[];
 
-    // Work item: row tiles fastest, last (longest) first.  Workgroups go round the XCDs; with eight key heads or
+    // Work item: splits fastest, then row tiles, last (longest) first, then heads.  Workgroups go round the XCDs; with eight key heads or
     // more each XCD takes a run of items, so that those that share keys share an L2 (with fewer heads a run would
     // hold long or short tiles only).
     const int total = a.tiles * a.c.kv_heads * a.splits, per = gridDim.x / XCDS;

@@ -36,7 +36,7 @@ void split_keys(Plan& p, int64_t alone, int64_t want, int64_t least, int max_len
 // rule NULL: a plan for the rule that needs most
 Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads, const pi_score_rule* rule) {
     Plan p{};
-    // keys that the rows of one sequence span
+    // keys that the rows of one sequence span (a prefix longer than the window leaves the rest to the last split)
     const int span = rule && rule->window > 0 ? (int)std::min<int64_t>(b->max_len, (int64_t)rule->window + b->max_new) : b->max_len;
     const int group = q_heads / c->kv_heads;
     p.most_rows = (int64_t)std::min(b->max_new, b->n_tokens) * group;
@@ -44,9 +44,13 @@ Plan plan_attention(const pi_kv_cache* c, const pi_seq_batch* b, int q_heads, co
     if (p.few) {
         p.tiles = b->n_seqs;
         p.rows = (int)p.most_rows;
-        // The chip holds 512 workgroups.  Few sequences are about alike, so two rounds do (one of 131072 tokens
-        // with 8 key heads: 89 us for 1024 workgroups, 97 for 2048, 105 for 3072); the lengths of many differ, and
-        // smaller pieces even them out (48 of 300 to 8191: 133, 104 and 94 us).
+        // The chip holds 512 workgroups.  One or two sequences are about alike, so two rounds do (one of 131072 tokens
+        // with 8 key heads: 89 us for 1024 workgroups, 97 for 2048, 105 for 3072); the lengths of many differ, and smaller
+        // pieces even them out.  Keys of 300 to 8191, 8 key heads of 128 f16, us for 1024, 2048 and 3072 workgroups:
+        //   4 sequences 19.3 19.4 19.3    5: 22.6 20.4 20.4    8: 26.8 29.0 28.9    16: 42.6 43.4 41.3
+        //   17: 49.0 48.6 43.7            32: 74.8 71.8 67.3   48: 131.7 103.9 94.8
+        // so both steps lie where the choice matters least.  What they cost if the lengths are alike after all (8000 keys
+        // each): 8 sequences 50.8 58.2 58.1, 16: 89.2 99.3 101.9, 48: 245 263 269.  The lengths are on the device.
         const int64_t want = b->n_seqs <= 4 ? 1024 : b->n_seqs <= 16 ? 2048 : 3072, alone = p.tiles * c->kv_heads;
         // A workgroup takes 3 to 4 us before its first key, the join 4: one piece up to 128 KB of keys (500 keys of 128
         // f16: 10.5 us against 12.3 in two), and the more workgroups there are, the longer the pieces (1000 keys,
