@@ -29,23 +29,24 @@ class PagedCache:
         self.v = torch.zeros(shape, dtype=dtype, device=device)
         i32 = dict(dtype=torch.int32, device=device)
         self.refs = torch.zeros(pages, **i32)
-        self.table = torch.full((max_seqs, -(-max_len // page_size)), -1, **i32)
-        self.lens = torch.zeros(max_seqs, **i32)
+        # one more row than sequences: the place of ids outside the table, which stays empty.  room is 1 where a
+        # sequence's last extension was granted
+        self._table = torch.full((max_seqs + 1, -(-max_len // page_size)), -1, **i32)
+        self._lens, self._room = torch.zeros(max_seqs + 1, **i32), torch.ones(max_seqs + 1, **i32)
+        self._room[max_seqs] = 0
+        self.table, self.lens = self._table[:max_seqs], self._lens[:max_seqs]
         self.cache = pb.make_kv_cache(self.k, self.v)
         self.state = pb.make_page_state(self.refs, self.table, self.lens, page_size)
         self.ws = torch.empty(pb.pi_pages_workspace_bytes(self.state, max_seqs),
                               dtype=torch.uint8, device=device)
         self.moved = torch.empty(pages, **i32)
-        # whether a sequence's last extension was granted; one more place, 0, for ids outside the table
-        self.room = torch.ones(max_seqs + 1, **i32)
-        self.room[max_seqs] = 0
 
     def ids(self, seqs: Sequence[int]) -> torch.Tensor:
         # from pinned memory, so that the copy is enqueued and not waited for
         return torch.tensor(list(seqs), dtype=torch.int32, pin_memory=True).to(self.device, non_blocking=True)
 
-    def _slots(self, seqs: torch.Tensor) -> torch.Tensor:
-        return torch.where((seqs >= 0) & (seqs < self.max_seqs), seqs, self.max_seqs).long()
+    def _rows(self, seqs: torch.Tensor) -> torch.Tensor:
+        return seqs.clamp(-1, self.max_seqs).long()      # (-1 is the last row too)
 
     def extend(self, seqs: torch.Tensor, add: torch.Tensor):
         """Room for add[i] more tokens in sequence seqs[i] (int32 device tensors); a shared last
@@ -55,7 +56,7 @@ class PagedCache:
         granted = torch.empty(n, dtype=torch.int32, device=self.device)
         copies = torch.empty((2, n), dtype=torch.int32, device=self.device)
         pb.pi_pages_extend(self.state, self.cache, seqs, add, granted, copies, self.ws)
-        self.room.scatter_(0, self._slots(seqs), granted)
+        self._room[self._rows(seqs)] = granted
         return granted, copies
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor):
@@ -79,11 +80,9 @@ class PagedCache:
         starts = [0]
         for n in new:
             starts.append(starts[-1] + n)
-        slot = self._slots(seqs)
-        at = slot.clamp_max(self.max_seqs - 1)
-        lens = torch.where(self.room[slot] > 0, self.lens[at], 0)
-        return pb.make_seq_batch(self.ids(starts), lens, self.table[at], starts[-1],
-                                 max(list(new) + [0]), max_len)
+        at = self._rows(seqs)
+        return pb.make_seq_batch(self.ids(starts), self._lens[at] * self._room[at], self._table[at],
+                                 starts[-1], max(list(new) + [0]), max_len)
 
 
 class AttentionLayer:
@@ -131,7 +130,7 @@ class DecoderLayer:
         if x.shape[0] == 0:
             return torch.empty_like(x)
         # as the FFN is now: a new index, a placement or a threshold replaces what the descriptors name
-        parts, predictor = self.ffn.parts(), self.ffn.predictor()
+        predictor, parts = self.ffn.descriptors()
         out = []
         for part in x.split(pb.PI_MAX_BATCH):
             n = part.shape[0]

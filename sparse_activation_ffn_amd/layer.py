@@ -60,6 +60,18 @@ class DeviceLayer:
                            c(self.P2t), c(self.b2), self.threshold, self.n_hot)
 
     # ---- descriptors ---------------------------------------------------------
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        self.__dict__.pop("_descriptors", None)
+
+    def descriptors(self):
+        """(predictor(), parts()), formed again after any of the layer's tensors, its split or
+        its threshold has been replaced (forming them takes the host 18 us)."""
+        kept = self.__dict__.get("_descriptors")
+        if kept is None:
+            kept = self.__dict__["_descriptors"] = (self.predictor(), self.parts())
+        return kept
+
     def predictor(self) -> pb.Predictor:
         return pb.make_predictor(self.P1t, self.P2t, self.b2, self.threshold)
 
