@@ -22,11 +22,13 @@ PI_RELU, PI_REGLU, PI_SQRELU = 0, 1, 2
 PI_MAX_BATCH = 64
 (PI_K_PRED_L1, PI_K_PRED_L2, PI_K_COMPACT, PI_K_UP, PI_K_DOWN, PI_K_MERGE, PI_K_PROFILE,
  PI_K_INDEX, PI_K_COPY, PI_K_REDUCE, PI_K_FFN, PI_K_ACCUMULATE, PI_K_STREAM, PI_K_UP_FINISH,
- PI_K_ROPE_APPEND, PI_K_ATTN, PI_K_ATTN_JOIN, PI_K_PAGES, PI_K_PAGE_COPY, PI_K_COUNT) = range(20)
+ PI_K_ROPE_APPEND, PI_K_ATTN, PI_K_ATTN_JOIN, PI_K_PAGES, PI_K_PAGE_COPY, PI_K_NORM,
+ PI_K_MX_CONVERT, PI_K_MX_PRODUCT, PI_K_MX_JOIN, PI_K_SAMPLE, PI_K_COUNT) = range(25)
 PI_STREAM_SINK_WORDS = 2048
 PI_SCRATCH_BYTES = 32 << 20
 PI_MAX_HEAD_DIM, PI_MAX_PAGE_SIZE = 256, 1024
 PI_ROPE_HALVES, PI_ROPE_PAIRS = 0, 1
+PI_MXFP8, PI_MXFP4 = 0, 1
 PI_SCALE_NONE, PI_SCALE_LINEAR, PI_SCALE_BASE, PI_SCALE_BANDS = range(4)
 
 # every symbol include/pi.h declares
@@ -42,6 +44,8 @@ EXPORTS = ("pi_workspace_bytes", "pi_workspace_init", "pi_predict", "pi_compact_
            "pi_rope_turns", "pi_rope_append", "pi_attention_workspace_bytes",
            "pi_paged_attention", "pi_pages_workspace_bytes", "pi_pages_extend", "pi_pages_fork",
            "pi_pages_free", "pi_pages_compact", "pi_pages_copy",
+           "pi_rms_norm", "pi_mx_quantize", "pi_mx_dequantize", "pi_mx_product_workspace_bytes",
+           "pi_mx_product", "pi_sample_workspace_bytes", "pi_sample",
            "pi_kernel_timer_start", "pi_kernel_timer_stop", "pi_kernel_name", "pi_status_string",
            "pi_last_error")
 
@@ -106,6 +110,20 @@ class PageState(C.Structure):
                 ("lens", C.c_void_p)]
 
 
+class Mx(C.Structure):
+    _fields_ = [("format", C.c_int32), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
+class Norm(C.Structure):
+    _fields_ = [("d", C.c_int32), ("wdtype", C.c_int32), ("weight", C.c_void_p), ("eps", C.c_float)]
+
+
+class SampleRule(C.Structure):
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p),
+                ("min_p", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -154,6 +172,13 @@ def lib() -> C.CDLL:
         "pi_pages_free": ([P, P, I32, P], I32),
         "pi_pages_compact": ([P, P, P, P, SZ, P], I32),
         "pi_pages_copy": ([P, P, P, I32, P], I32),
+        "pi_rms_norm": ([P, I32, I32, I32, P, I32, P, P, P, P, P], I32),
+        "pi_mx_quantize": ([P, I64, I32, P, P], I32),
+        "pi_mx_dequantize": ([P, P, I64, I32, P], I32),
+        "pi_mx_product_workspace_bytes": ([I32, I32, I32], SZ),
+        "pi_mx_product": ([P, P, P, P, I64, I32, P, SZ, P], I32),
+        "pi_sample_workspace_bytes": ([I32, I32], SZ),
+        "pi_sample": ([P, I32, I32, I64, I32, P, P, P, P, P, P, SZ, P], I32),
         "pi_kernel_timer_start": ([I32, I32], I32),
         "pi_kernel_timer_stop": ([I32, P, P], I32),
         "pi_kernel_name": ([I32], C.c_char_p),
@@ -445,6 +470,70 @@ def pi_pages_copy(cache: KvCache, src, dst, stream=None):
                                stream_handle(stream)))
 
 
+# ---- norms, microscaled products, sampling ------------------------------------------
+
+def pi_rms_norm(norm: Norm, x, delta=None, sum_out=None, y=None, mx: Optional[Mx] = None, stream=None):
+    """x, delta, sum_out, y: [tokens][d] or [tokens][heads][d], the elements of a row contiguous, other strides free;
+    sum_out and y of x's dtype, delta float32 or float16."""
+    shape, dt = x.shape, dtype_code(x)
+    parts = [_norm_rows(name, t, shape, norm.d, None if name == "delta" else dt)
+             for name, t in (("x", x), ("delta", delta), ("sum_out", sum_out), ("y", y))]
+    heads = 1 if len(shape) == 2 else shape[1]
+    _on_device(getattr(norm, "_keep", None), x, delta, sum_out, y, *getattr(mx, "_keep", ()))
+    _check(lib().pi_rms_norm(C.byref(norm), shape[0], heads, dt, parts[0], 0 if delta is None else dtype_code(delta),
+                             parts[1], parts[2], parts[3], None if mx is None else C.byref(mx),
+                             stream_handle(stream)))
+
+
+def pi_mx_quantize(x, mx: Mx, stream=None):
+    """x [mx.rows][mx.cols], the elements of a row contiguous."""
+    _matrix("x", x, mx.rows, mx.cols)
+    _on_device(x, *getattr(mx, "_keep", ()))
+    _check(lib().pi_mx_quantize(ptr(x), x.stride(0), dtype_code(x), C.byref(mx), stream_handle(stream)))
+
+
+def pi_mx_dequantize(mx: Mx, out, stream=None):
+    """out [mx.rows][mx.cols], the elements of a row contiguous."""
+    _matrix("out", out, mx.rows, mx.cols)
+    _on_device(out, *getattr(mx, "_keep", ()))
+    _check(lib().pi_mx_dequantize(C.byref(mx), ptr(out), out.stride(0), dtype_code(out), stream_handle(stream)))
+
+
+def pi_mx_product_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(lib().pi_mx_product_workspace_bytes(m, n, k))
+
+
+def pi_mx_product(a: Mx, w: Mx, out, bias=None, ws=None, stream=None):
+    """out [a.rows][w.rows], the elements of a row contiguous; bias float32 [w.rows] or None; ws of
+    pi_mx_product_workspace_bytes(a.rows, w.rows, a.cols) bytes."""
+    _matrix("out", out, a.rows, w.rows)
+    _vector("bias", bias, "float32", w.rows)
+    _on_device(out, bias, ws, *getattr(a, "_keep", ()), *getattr(w, "_keep", ()))
+    _check(lib().pi_mx_product(C.byref(a), C.byref(w), ptr(bias), ptr(out), out.stride(0), dtype_code(out), ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
+
+
+def pi_sample_workspace_bytes(rows: int, vocab: int) -> int:
+    return int(lib().pi_sample_workspace_bytes(rows, vocab))
+
+
+def pi_sample(logits, rule: SampleRule, u, token, prob=None, kept=None, ws=None, stream=None):
+    """logits [rows][vocab], the elements of a row contiguous; u float32 [rows]; token int32 [rows], prob float32
+    [rows], kept int32 [rows] (the last two may be None)."""
+    rows, vocab = logits.shape
+    _matrix("logits", logits, rows, vocab)
+    for name, t, dtype in (("u", u, "float32"), ("token", token, "int32"), ("prob", prob, "float32"),
+                           ("kept", kept, "int32")):
+        _vector(name, t, dtype, rows)
+    for t in getattr(rule, "_keep", ()):
+        if t is not None and not isinstance(t, int) and t.numel() < rows:
+            raise ValueError(f"a rule's list has {t.numel()} entries for {rows} rows")
+    _on_device(logits, u, token, prob, kept, ws, *getattr(rule, "_keep", ()))
+    _check(lib().pi_sample(ptr(logits), rows, vocab, logits.stride(0), dtype_code(logits), C.byref(rule), ptr(u),
+                           ptr(token), ptr(prob), ptr(kept), ptr(ws),
+                           0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
+
+
 def pi_kernel_timer_start(kid: int, max_launches: int):
     _check(lib().pi_kernel_timer_start(kid, max_launches))
 
@@ -539,6 +628,81 @@ def make_page_state(refs, table, lens, page_size: int) -> PageState:
     s = PageState(refs.numel(), n, table.shape[-1], page_size, ptr(refs), ptr(table), ptr(lens))
     s._keep = (refs, table, lens)
     return s
+
+
+def make_norm(weight, eps: float = 1e-5, d: int = 0) -> Norm:
+    """weight [d] float32 or float16, or None with d given (a norm without weights)."""
+    if weight is None:
+        return Norm(d, 0, None, float(eps))
+    if len(weight.shape) != 1 or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous vector")
+    n = Norm(weight.numel(), dtype_code(weight), ptr(weight), float(eps))
+    n._keep = weight
+    return n
+
+
+def make_mx(codes, scales, fmt: int) -> Mx:
+    """codes uint8 [rows][cols] (PI_MXFP8) or [rows][cols / 2] (PI_MXFP4), scales uint8 [rows][cols / 32]."""
+    import torch
+    rows, cols = codes.shape
+    if fmt == PI_MXFP4:
+        cols *= 2
+    for name, t in (("codes", codes), ("scales", scales)):
+        if t.dtype is not torch.uint8 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 tensor")
+    if cols % 32 or tuple(scales.shape) != (rows, cols // 32):
+        raise ValueError(f"codes {tuple(codes.shape)} need scales [{rows}][cols / 32], cols a multiple of 32; "
+                         f"got {tuple(scales.shape)}")
+    m = Mx(fmt, rows, cols, ptr(codes), ptr(scales))
+    m._keep = (codes, scales)
+    return m
+
+
+def empty_mx(rows: int, cols: int, fmt: int, device="cuda") -> Mx:
+    """A matrix to quantise into."""
+    import torch
+    u8 = dict(dtype=torch.uint8, device=device)
+    return make_mx(torch.empty((rows, cols // 2 if fmt == PI_MXFP4 else cols), **u8),
+                   torch.empty((rows, cols // 32), **u8), fmt)
+
+
+def make_sample_rule(temperature=None, top_k=None, top_p=None, min_p=None) -> SampleRule:
+    """Lists with an entry per row (device tensors: float32, top_k int32), or None."""
+    _vector("temperature", temperature, "float32", 0)
+    _vector("top_k", top_k, "int32", 0)
+    _vector("top_p", top_p, "float32", 0)
+    _vector("min_p", min_p, "float32", 0)
+    r = SampleRule(ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p))
+    r._keep = (temperature, top_k, top_p, min_p)
+    return r
+
+
+def _matrix(name: str, t, rows: int, cols: int):
+    if len(t.shape) != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}][{cols}] with contiguous rows, got {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+
+
+def _norm_rows(name: str, t, shape, d: int, dtype):
+    """Reference to [tokens][d] or [tokens][heads][d] as the library sees it, or None."""
+    if t is None:
+        return None
+    strides = t.stride()
+    if len(shape) not in (2, 3) or t.shape != shape or shape[-1] != d or (d > 1 and strides[-1] != 1):
+        raise ValueError(f"{name} must be [tokens]([heads])[{d}] like x {tuple(shape)} with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {strides}")
+    if dtype is not None and dtype_code(t) != dtype:
+        raise TypeError(f"{name} has x's dtype")
+    return C.byref(Rows(t.data_ptr(), strides[0], strides[1] if len(shape) == 3 else 0))
+
+
+def _on_device(*tensors):
+    """Refuses tensors (None and addresses pass) that are not on the current device: a kernel on its stream would fault."""
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != here:
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{here}")
 
 
 def _int32(name: str, t, shape):

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpi.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("pi_api.hip", "pi_attn.hip", "pi_pages.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("pi_api.hip", "pi_attn.hip", "pi_pages.hip", "pi_norm.hip",
+                                              "pi_mx.hip", "pi_sample.hip")]
 # host-core code of the hybrid step: built by the host compiler, linked in
 HOST_SOURCES = [os.path.join(CSRC, "pi_host.cpp")]
 DEPS = SOURCES + HOST_SOURCES + \

@@ -683,7 +683,8 @@ const char* pi_kernel_name(int32_t kid) {
                                             "k_merge", "k_profile", "k_index", "k_copy", "k_reduce",
                                             "k_ffn", "k_accumulate_mask", "k_stream_read",
                                             "k_up_finish", "k_rope_append", "k_attn", "k_attn_join", "k_pages",
-                                            "k_page_copy"};
+                                            "k_page_copy", "k_rms_norm", "k_mx_convert", "k_mx_product",
+                                            "k_mx_join", "k_sample"};
     return (kid >= 0 && kid < PI_K_COUNT) ? names[kid] : "?";
 }
 

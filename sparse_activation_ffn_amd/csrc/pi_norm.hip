@@ -1,0 +1,440 @@
+// pi_norm.hip -- the residual's addition with a root-mean-square norm, and
+// microscaled quantisation and its inverse.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "pi.h"
+#include "pi_cache.h"
+#include "pi_launch.h"
+#include "pi_mx.h"
+
+using namespace pi;
+
+namespace {
+
+constexpr int NT = 256;        // threads of a workgroup
+constexpr int NONE = -1;       // no delta, no weight, no microscaled output
+
+struct NormArgs {
+    const uint8_t* x;
+    const uint8_t* delta;
+    uint8_t* sum;
+    uint8_t* y;
+    uint8_t* codes;
+    uint8_t* scales;
+    const uint8_t* weight;
+    int64_t x_ts, x_hs, d_ts, d_hs, s_ts, s_hs, y_ts, y_hs;   // strides in bytes
+    double eps;
+    int rows, heads, d;
+    int ddtype, wdtype, format;                               // or NONE
+};
+
+// ---- the norm ----------------------------------------------------------------------
+//
+// s = x + delta; y = s w / sqrt(mean(s^2) + eps).  Every input and output byte moves once, some ten operations an
+// element: the HBM rate bounds it, a launch and two dependent latencies where there are few rows.  So a row stays in
+// registers between the sum of its squares and its outputs: 8 elements (a 16-byte load of f16) per thread and chunk, a
+// row on 8 to 64 lanes of a wave (heads) or on a workgroup.  The squares are summed in 64 bits: exact products of
+// f16, and no overflow for float32.
+
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)b, CTRL, 0xf, 0xf, false);
+    const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), CTRL, 0xf, 0xf, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// the sum over LANES consecutive lanes, in every one of them
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double v) {
+    v = add_dpp<DPP_QUAD_1032>(v);
+    v = add_dpp<DPP_QUAD_2301>(v);
+    v = add_dpp<DPP_ROW_HALF_MIRROR>(v);
+    if constexpr (LANES >= 16) v = add_dpp<DPP_ROW_MIRROR>(v);
+    if constexpr (LANES >= 32) v += __shfl_xor(v, 16);
+    if constexpr (LANES >= 64) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// the sum over the whole workgroup
+__device__ __forceinline__ double workgroup_sum(double v, double* lds) {
+    v = lanes_sum<64>(v);
+    if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+template <int XT>
+__device__ __forceinline__ float rounded(float v) {
+    return XT == F16 ? (float)(_Float16)v : v;
+}
+
+__device__ __forceinline__ float element(const uint8_t* p, int dtype, int i) {
+    return dtype == F16 ? (float)reinterpret_cast<const _Float16*>(p)[i] : reinterpret_cast<const float*>(p)[i];
+}
+
+// The float32 next to a value, y its nearest and rest = value - y, whose last bit is 1 unless the value is y: rounded on
+// to fewer bits, it gives what the value itself would.
+__device__ __forceinline__ float to_odd(float y, float rest) {
+    unsigned b = __builtin_bit_cast(unsigned, y);
+    if (rest < 0.0f ? y > 0.0f : rest > 0.0f && y < 0.0f) --b;
+    return __builtin_bit_cast(float, b | (rest != 0.0f ? 1u : 0u));
+}
+
+// y of one element, as the nearest float32 and to odd.  f16 times f16 is exact in float32, so with r as a sum of two floats
+// one rounding is left, and its rest is known; the other forms go through 64 bits, which costs nothing at the HBM rate.
+struct Scale {
+    double r;
+    float hi, lo;
+    __device__ explicit Scale(double mean_eps) : r(1.0 / sqrt(mean_eps)), hi((float)r), lo((float)(r - (double)hi)) {}
+    template <bool EXACT>
+    __device__ __forceinline__ float of(float s, float w, float& odd) const {
+        float y, rest;
+        if constexpr (EXACT) {
+            const float t = s * w;
+            const float low = fabsf(t) < INFINITY ? t * lo : 0.0f;   // (an infinite weight meets lo of either sign)
+            y = fmaf(t, hi, low);
+            rest = fmaf(t, hi, -y) + low;
+        } else {
+            const double v = (double)s * r * (double)w;
+            y = (float)v;
+            rest = (float)(v - (double)y);
+        }
+        odd = to_odd(y, fabsf(y) < INFINITY ? rest : 0.0f);
+        return y;
+    }
+};
+
+// TPR threads to a row, C chunks of 8 elements to a thread.  d % 8 == 0 and every row 16-byte aligned.
+template <int XT, int TPR, int C>
+__global__ __launch_bounds__(NT) void k_rms_norm(NormArgs a) {
+    constexpr int PER = NT / TPR;                        // rows of a workgroup
+    __shared__ double lds[NT / WAVE];
+    const int t = threadIdx.x % TPR;
+    const int row = blockIdx.x * PER + threadIdx.x / TPR;
+    if (PER > 1 && row >= a.rows) return;                // (whole groups of lanes that work together)
+    const int token = a.heads == 1 ? row : row / a.heads, head = row - token * a.heads;
+    constexpr int ES = XT == F16 ? 2 : 4;
+    const uint8_t* x = a.x + token * a.x_ts + head * a.x_hs;
+    const uint8_t* delta = a.delta + token * a.d_ts + head * a.d_hs;
+    float s[C][8];
+    double squares = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+        if (at < a.d) {
+            load8<XT, true>(x + (int64_t)at * ES, s[c]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[c][e] = 0.0f;
+        }
+    }
+    if (a.ddtype != NONE) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = (c * TPR + t) * 8;
+            if (at < a.d) {
+                float dv[8];
+                if (a.ddtype == F16)
+                    load8<F16, true>(delta + (int64_t)at * 2, dv);
+                else
+                    load8<F32, true>(delta + (int64_t)at * 4, dv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[c][e] = rounded<XT>(s[c][e] + dv[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) squares = fma((double)s[c][e], (double)s[c][e], squares);
+    double total;
+    if constexpr (TPR <= WAVE)
+        total = lanes_sum<TPR>(squares);
+    else
+        total = workgroup_sum(squares, lds);
+    const Scale scale(total / a.d + a.eps);
+    uint8_t* sum = a.sum + token * a.s_ts + head * a.s_hs;
+    uint8_t* y = a.y + token * a.y_ts + head * a.y_hs;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+        if (at >= a.d) continue;
+        if (a.sum) store8<XT, true>(sum + (int64_t)at * ES, s[c]);
+        float w[8], v[8], odd[8];
+        if (a.wdtype == F16)
+            load8<F16, true>(a.weight + (int64_t)at * 2, w);
+        else if (a.wdtype == F32)
+            load8<F32, true>(a.weight + (int64_t)at * 4, w);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        if (XT == F16 && a.wdtype != F32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = scale.of<true>(s[c][e], w[e], odd[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = scale.of<false>(s[c][e], w[e], odd[e]);
+        }
+        if (a.y) store8<XT, true>(y + (int64_t)at * ES, XT == F16 ? odd : v);
+        const int64_t in_all = (int64_t)row * a.d + at;
+        if (a.format == PI_MXFP8)
+            store_block<PI_MXFP8>(odd, in_all, a.codes, a.scales);
+        else if (a.format == PI_MXFP4)
+            store_block<PI_MXFP4>(odd, in_all, a.codes, a.scales);
+    }
+}
+
+// Any size and alignment: a workgroup per row, an element per thread and step, the row read again from the caches.
+template <int XT>
+__global__ __launch_bounds__(NT) void k_rms_norm_any(NormArgs a) {
+    typedef typename std::conditional<XT == F16, _Float16, float>::type T;
+    __shared__ double lds[NT / WAVE];
+    const int row = blockIdx.x;
+    const int token = row / a.heads, head = row - token * a.heads;
+    const T* x = reinterpret_cast<const T*>(a.x + token * a.x_ts + head * a.x_hs);
+    const uint8_t* delta = a.delta + token * a.d_ts + head * a.d_hs;
+    T* sum = reinterpret_cast<T*>(a.sum + token * a.s_ts + head * a.s_hs);
+    T* y = reinterpret_cast<T*>(a.y + token * a.y_ts + head * a.y_hs);
+    double squares = 0.0;
+    for (int i = threadIdx.x; i < a.d; i += NT) {
+        float s = (float)x[i];
+        if (a.ddtype != NONE) s = rounded<XT>(s + element(delta, a.ddtype, i));
+        if (a.sum) sum[i] = (T)s;
+        squares = fma((double)s, (double)s, squares);
+    }
+    const Scale scale(workgroup_sum(squares, lds) / a.d + a.eps);
+    for (int i = threadIdx.x; i < a.d; i += NT) {
+        // (a sum may have replaced x or delta; this thread wrote it)
+        float s = a.sum ? (float)sum[i] : (float)x[i];
+        if (!a.sum && a.ddtype != NONE) s = rounded<XT>(s + element(delta, a.ddtype, i));
+        const float w = a.wdtype == NONE ? 1.0f : element(a.weight, a.wdtype, i);
+        float odd;
+        const float v = scale.of<false>(s, w, odd);
+        if (a.y) y[i] = (T)(XT == F16 ? odd : v);
+        if (a.format != NONE) {
+            // d % 32 == 0: 32 lanes hold a block
+            unsigned top = magnitude_bits(odd);
+#pragma unroll
+            for (int m = 1; m < 32; m *= 2) top = max(top, (unsigned)__shfl_xor((int)top, m));
+            const int64_t in_all = (int64_t)row * a.d + i;
+            const float v8[8] = {odd, 0, 0, 0, 0, 0, 0, 0};
+            int e;
+            if (a.format == PI_MXFP8) {
+                e = block_exponent<PI_MXFP8>(top);
+                a.codes[in_all] = (uint8_t)mx_codes<PI_MXFP8>(v8, e).x;
+            } else {
+                e = block_exponent<PI_MXFP4>(top);
+                const unsigned c = mx_codes<PI_MXFP4>(v8, e).x & 15u, next = __shfl_xor((int)c, 1);
+                if (i % 2 == 0) a.codes[in_all / 2] = (uint8_t)(c | next << 4);
+            }
+            if (i % 32 == 0) a.scales[in_all / 32] = scale_byte(top, e);
+        }
+    }
+}
+
+// ---- microscaled quantisation ----------------------------------------------------------
+//
+// Bytes alone bound both directions.  A thread takes 8 elements, a quad of lanes a block; 2^log lanes a row, so that
+// short rows fill a wave.
+struct ConvertArgs {
+    const uint8_t* x;
+    uint8_t* out;
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t stride;            // of x or out, in bytes
+    int rows, cols, log;
+};
+
+template <int XT, int FMT, bool VEC>
+__global__ __launch_bounds__(NT) void k_mx_quantize(ConvertArgs a) {
+    constexpr int ES = XT == F16 ? 2 : 4;
+    const int at = ((int)blockIdx.y << a.log | (int)(threadIdx.x & ((1u << a.log) - 1))) * 8;
+    if (at >= a.cols) return;
+    const int per = NT >> a.log;
+    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += gridDim.x * per) {
+        float v[8];
+        load8<XT, VEC>(a.x + row * a.stride + (int64_t)at * ES, v);
+        store_block<FMT>(v, (int64_t)row * a.cols + at, a.codes, a.scales);
+    }
+}
+
+template <int XT, int FMT, bool VEC>
+__global__ __launch_bounds__(NT) void k_mx_dequantize(ConvertArgs a) {
+    constexpr int ES = XT == F16 ? 2 : 4;
+    const int at = ((int)blockIdx.y << a.log | (int)(threadIdx.x & ((1u << a.log) - 1))) * 8;
+    if (at >= a.cols) return;
+    const int per = NT >> a.log;
+    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += gridDim.x * per) {
+        const int64_t in_all = (int64_t)row * a.cols + at;
+        float v[8];
+        if constexpr (FMT == PI_MXFP8) {
+            const u2 c = *reinterpret_cast<const u2*>(a.codes + in_all);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto p = i % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i / 2], true)
+                                     : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i / 2], false);
+                v[2 * i] = p[0], v[2 * i + 1] = p[1];
+            }
+        } else {
+            const unsigned c = *reinterpret_cast<const unsigned*>(a.codes + in_all / 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c >> (8 * i), 1.0f, 0);
+                v[2 * i] = p[0], v[2 * i + 1] = p[1];
+            }
+        }
+        const int scale = a.scales[in_all / 32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = scale == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[i], scale - 127);
+        store8<XT, VEC>(a.out + row * a.stride + (int64_t)at * ES, v);
+    }
+}
+
+template <bool QUANTIZE, int XT, int FMT, bool VEC>
+pi_status launch_convert(const ConvertArgs& a, hipStream_t s) {
+    const int per = NT >> a.log;
+    const dim3 grid(std::min((a.rows + per - 1) / per, 1 << 16), ((a.cols / 8) + (1 << a.log) - 1) >> a.log);
+    if constexpr (QUANTIZE)
+        return launch(PI_K_MX_CONVERT, k_mx_quantize<XT, FMT, VEC>, grid, dim3(NT), 0, s, a);
+    else
+        return launch(PI_K_MX_CONVERT, k_mx_dequantize<XT, FMT, VEC>, grid, dim3(NT), 0, s, a);
+}
+
+template <bool QUANTIZE>
+pi_status convert(const void* data, int64_t stride, int dtype, const pi_mx* mx, hipStream_t s) {
+    const int size = dtype_size(dtype);
+    ConvertArgs a{};
+    a.x = (const uint8_t*)data;
+    a.out = QUANTIZE ? nullptr : (uint8_t*)const_cast<void*>(data);
+    a.codes = (uint8_t*)mx->codes, a.scales = mx->scales;
+    a.stride = stride * size;
+    a.rows = mx->rows, a.cols = mx->cols;
+    a.log = 2;
+    while (a.log < 8 && (1 << a.log) < mx->cols / 8) ++a.log;
+    const bool vec = aligned(data, 16) && (mx->rows == 1 || a.stride % 16 == 0);
+    const bool f16 = dtype == PI_F16, fp8 = mx->format == PI_MXFP8;
+#define GO(XT, FMT) (vec ? launch_convert<QUANTIZE, XT, FMT, true>(a, s) : launch_convert<QUANTIZE, XT, FMT, false>(a, s))
+    return f16 ? (fp8 ? GO(F16, PI_MXFP8) : GO(F16, PI_MXFP4)) : (fp8 ? GO(F32, PI_MXFP8) : GO(F32, PI_MXFP4));
+#undef GO
+}
+
+pi_status check_matrix(const void* data, int64_t stride, int dtype, const pi_mx* mx, const char* name, bool out) {
+    TRY(check_mx(mx, "mx"));
+    TRY(check_elem_dtype(dtype, name));
+    if (mx->rows == 0) return PI_OK;
+    CHECK(data, PI_ERR_ARG, "%s is required", name);
+    CHECK(aligned(data, dtype_size(dtype)), PI_ERR_ALIGN, "%s must be aligned to its elements", name);
+    CHECK(stride >= (out && mx->rows > 1 ? mx->cols : 0) && stride < ((int64_t)1 << 40), PI_ERR_SHAPE,
+          "%s: row_stride must be in %s..2^40", name, out ? "cols" : "0");
+    return PI_OK;
+}
+
+// ---- the norm's entry point ---------------------------------------------------------
+
+template <int XT, int TPR, int C>
+pi_status launch_norm(const NormArgs& a, hipStream_t s) {
+    constexpr int PER = NT / TPR;
+    return launch(PI_K_NORM, k_rms_norm<XT, TPR, C>, dim3((a.rows + PER - 1) / PER), dim3(NT), 0, s, a);
+}
+
+template <int XT>
+pi_status norm_by_size(const NormArgs& a, bool vec, hipStream_t s) {
+    if (!vec || a.d > 8 * NT * 8)
+        return launch(PI_K_NORM, k_rms_norm_any<XT>, dim3(a.rows), dim3(NT), 0, s, a);
+    if (a.d <= 64) return launch_norm<XT, 8, 1>(a, s);
+    if (a.d <= 128) return launch_norm<XT, 16, 1>(a, s);
+    if (a.d <= 256) return launch_norm<XT, 32, 1>(a, s);
+    if (a.d <= 512) return launch_norm<XT, 64, 1>(a, s);
+    if (a.d <= 8 * NT) return launch_norm<XT, NT, 1>(a, s);
+    if (a.d <= 8 * NT * 2) return launch_norm<XT, NT, 2>(a, s);
+    if (a.d <= 8 * NT * 4) return launch_norm<XT, NT, 4>(a, s);
+    return launch_norm<XT, NT, 8>(a, s);
+}
+
+// rows of an operand, and whether all of them are 16-byte aligned
+pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, int tokens, int heads, bool out, bool& vec) {
+    const int size = dtype_size(dtype);
+    CHECK(r->data, PI_ERR_ARG, "%s is required", name);
+    CHECK(aligned(r->data, size), PI_ERR_ALIGN, "%s must be aligned to its elements", name);
+    CHECK(r->token_stride >= 0 && r->head_stride >= 0 && r->token_stride < ((int64_t)1 << 40) &&
+              r->head_stride < ((int64_t)1 << 40),
+          PI_ERR_SHAPE, "%s: strides must be in 0..2^40", name);
+    CHECK(!out || ((tokens == 1 || r->token_stride >= d) && (heads == 1 || r->head_stride >= d)), PI_ERR_SHAPE,
+          "%s: rows that are written may not overlap", name);
+    vec = vec && aligned(r->data, 16) && (tokens == 1 || r->token_stride * size % 16 == 0) &&
+          (heads == 1 || r->head_stride * size % 16 == 0);
+    return PI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_t dtype, const pi_rows* x, int32_t ddtype,
+                      const pi_rows* delta, const pi_rows* sum, const pi_rows* y, const pi_mx* mx, void* stream) {
+    CHECK(norm, PI_ERR_ARG, "NULL norm");
+    CHECK(norm->d >= 1 && norm->d <= (1 << 20), PI_ERR_SHAPE, "norm: d must be in 1..2^20");
+    CHECK(norm->eps >= 0.0f && std::isfinite(norm->eps), PI_ERR_ARG, "norm: eps must be finite and not negative");
+    CHECK(tokens >= 0 && heads >= 1 && (int64_t)tokens * heads <= (1 << 23), PI_ERR_SHAPE,
+          "norm: heads must be >= 1 and tokens * heads in 0..2^23");
+    TRY(check_elem_dtype(dtype, "norm"));
+    const int d = norm->d;
+    bool vec = d % 8 == 0;
+    if (norm->weight) {
+        TRY(check_elem_dtype(norm->wdtype, "norm: weight"));
+        CHECK(aligned(norm->weight, dtype_size(norm->wdtype)), PI_ERR_ALIGN, "norm: weight must be aligned to its elements");
+        vec = vec && aligned(norm->weight, 16);
+    }
+    CHECK(sum || y || mx, PI_ERR_ARG, "norm: one of sum, y and mx is required");
+    CHECK(delta || !sum, PI_ERR_ARG, "norm: sum without delta");
+    if (delta) TRY(check_elem_dtype(ddtype, "norm: delta"));
+    if (mx) {
+        TRY(check_mx(mx, "mx"));
+        CHECK(d % 32 == 0, PI_ERR_SHAPE, "norm: d must be a multiple of 32 for mx");
+        CHECK(mx->rows == tokens && mx->cols == (int64_t)heads * d, PI_ERR_SHAPE, "norm: mx must be [tokens][heads * d]");
+    }
+    if (tokens == 0) return PI_OK;
+    CHECK(x, PI_ERR_ARG, "x is required");
+    NormArgs a{};
+    const int size = dtype_size(dtype);
+    TRY(check_norm_rows(x, "x", dtype, d, tokens, heads, false, vec));
+    a.x = (const uint8_t*)x->data, a.x_ts = x->token_stride * size, a.x_hs = x->head_stride * size;
+    a.ddtype = a.wdtype = a.format = NONE;
+    if (delta) {
+        TRY(check_norm_rows(delta, "delta", ddtype, d, tokens, heads, false, vec));
+        a.ddtype = ddtype;
+        a.delta = (const uint8_t*)delta->data;
+        a.d_ts = delta->token_stride * dtype_size(ddtype), a.d_hs = delta->head_stride * dtype_size(ddtype);
+    }
+    if (sum) {
+        TRY(check_norm_rows(sum, "sum", dtype, d, tokens, heads, true, vec));
+        a.sum = (uint8_t*)sum->data, a.s_ts = sum->token_stride * size, a.s_hs = sum->head_stride * size;
+    }
+    if (y) {
+        TRY(check_norm_rows(y, "y", dtype, d, tokens, heads, true, vec));
+        a.y = (uint8_t*)y->data, a.y_ts = y->token_stride * size, a.y_hs = y->head_stride * size;
+        CHECK(!sum || sum->data != y->data, PI_ERR_ARG, "norm: sum and y must differ");
+    }
+    if (mx) a.format = mx->format, a.codes = (uint8_t*)mx->codes, a.scales = mx->scales;
+    if (norm->weight) a.wdtype = norm->wdtype, a.weight = (const uint8_t*)norm->weight;
+    a.eps = norm->eps;
+    a.rows = tokens * heads, a.heads = heads, a.d = d;
+    return dtype == PI_F16 ? norm_by_size<F16>(a, vec, (hipStream_t)stream) : norm_by_size<F32>(a, vec, (hipStream_t)stream);
+}
+
+pi_status pi_mx_quantize(const void* x, int64_t row_stride, int32_t dtype, const pi_mx* mx, void* stream) {
+    TRY(check_matrix(x, row_stride, dtype, mx, "x", false));
+    return mx->rows == 0 ? PI_OK : convert<true>(x, row_stride, dtype, mx, (hipStream_t)stream);
+}
+
+pi_status pi_mx_dequantize(const pi_mx* mx, void* out, int64_t row_stride, int32_t dtype, void* stream) {
+    TRY(check_matrix(out, row_stride, dtype, mx, "out", true));
+    return mx->rows == 0 ? PI_OK : convert<false>(out, row_stride, dtype, mx, (hipStream_t)stream);
+}
+
+}  // extern "C"
