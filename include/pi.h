@@ -754,6 +754,7 @@ pi_status pi_mx_dequantize(const pi_mx* mx, void* out, int64_t row_stride, int32
  * below the largest of them; outputs are off by some 2^-16 of their usual size, f16's
  * own rounding being 2^-12.  A NaN in a row of a or w reaches the outputs that it takes
  * part in, and no others; sums past float32 are infinite.
+ * Refused (PI_ERR_SHAPE) past 2^23 tiles of 128 x 128 outputs.
  * Needs a workspace of pi_mx_product_workspace_bytes(m, n, k) bytes for m = a->rows,
  * n = w->rows, k = cols (256-byte aligned; 0 bytes: none; a call with fewer rows of a
  * needs no more than one with more).

@@ -244,7 +244,8 @@ def check_product(a, w, fa, got, bias=None):
 
 PRODUCTS = [(1, 64, 32), (1, 1, 32), (1, 100, 1024), (2, 33, 96), (3, 7168, 160), (15, 200, 512), (16, 1024, 1024), (17, 17, 544),
             (33, 130, 7168), (48, 500, 2048), (64, 256, 8192), (65, 257, 1056), (100, 129, 480), (129, 1000, 640), (200, 300, 288),
-            (256, 256, 256), (257, 513, 384), (300, 1025, 1536), (513, 260, 128), (1, 4099, 12288), (1000, 700, 64)]
+            (256, 256, 256), (257, 513, 384), (300, 1025, 1536), (513, 260, 128), (1, 4099, 12288), (1000, 700, 64),
+            (5, 8300, 1056), (16, 8192, 512), (20, 400, 2080), (200, 300, 4128), (130, 257, 3584)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
@@ -259,6 +260,21 @@ def test_product(m, n, k, fa):
     a16 = (a[0], (a[1] - 12).astype(np.uint8)) if fa == "fp8" else a
     check_product(a16, w, fa, run_product(a16, w, fa, out="f16", pad=(-n) % 8), None)
     check_product(a16, w, fa, run_product(a16, w, fa, bias, out="f16", pad=3, off=1), bias.astype(np.float64))
+
+
+@pytest.mark.parametrize("fa", ["fp8", "fp4"])
+def test_product_of_many_tiles(fa):
+    """Outputs in hundreds of tiles, odd sizes: some rows of them."""
+    m, n, k = 2177, 4001, 672
+    rng = np.random.default_rng(9)
+    a, w = random_mx(rng, m, k, fa), random_mx(rng, n, k, "fp4")
+    if fa == "fp8":
+        a = (a[0], (a[1] - 12).astype(np.uint8))
+    bias = rng.standard_normal(n).astype(np.float32) * 100
+    rows = np.unique(np.concatenate([[0, 15, 16, 63, 64, 127, 128, 129, 2047, 2048, 2175, m - 1], rng.integers(0, m, 20)]))
+    some = (a[0][rows], a[1][rows])
+    check_product(some, w, fa, run_product(a, w, fa, bias, pad=3)[rows], bias.astype(np.float64))
+    check_product(some, w, fa, run_product(a, w, fa, out="f16", pad=7)[rows])
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 40, 160), (20, 40, 544), (150, 280, 1056)])
