@@ -386,11 +386,38 @@ __global__ __launch_bounds__(WAVE * WM * WN, 2) void k_mx_many(ProductArgs p) {
         const int row = min(wave * T::LW + i, T::NW - 1) * (1024 / T::RW) + lane / (T::RW / 16);
         w_off[i] = (unsigned)min(row, p.n - 1 - n0) * wb + piece_of<T::RW>(row, lane % (T::RW / 16)) * 16;
     }
+    // (of a last stage that is cut, lanes whose pieces are past the row's end read its first ones again: all waves have to
+    // have as many loads in flight; clear_stage clears what they got)
     auto load_stage = [&](int k, uint8_t* __restrict__ to) __attribute__((always_inline)) {
+        const int ak = k / (WIDE ? 1 : 2), wk = k / 2;
+        if (!ALIGNED && k + KS > p.k) {
 #pragma unroll
-        for (int i = 0; i < T::LA; ++i) load_to_lds(a + (k / (WIDE ? 1 : 2)) + a_off[i], to + min(wave * T::LA + i, T::NA - 1) * 1024);
+            for (int i = 0; i < T::LA; ++i) {
+                const int q = min(wave * T::LA + i, T::NA - 1), row = q * (1024 / T::RA) + lane / (T::RA / 16);
+                const int at = ak + piece_of<T::RA>(row, lane % (T::RA / 16)) * 16;
+                load_to_lds(a + ((unsigned)min(row, p.m - 1 - m0) * ab + (at < ab ? at : 0)), to + q * 1024);
+            }
 #pragma unroll
-        for (int i = 0; i < T::LW; ++i) load_to_lds(w + k / 2 + w_off[i], to + T::A_BYTES + min(wave * T::LW + i, T::NW - 1) * 1024);
+            for (int i = 0; i < T::LW; ++i) {
+                const int q = min(wave * T::LW + i, T::NW - 1), row = q * (1024 / T::RW) + lane / (T::RW / 16);
+                const int at = wk + piece_of<T::RW>(row, lane % (T::RW / 16)) * 16;
+                load_to_lds(w + ((unsigned)min(row, p.n - 1 - n0) * wb + (at < wb ? at : 0)), to + T::A_BYTES + q * 1024);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < T::LA; ++i) load_to_lds(a + ak + a_off[i], to + min(wave * T::LA + i, T::NA - 1) * 1024);
+#pragma unroll
+        for (int i = 0; i < T::LW; ++i) load_to_lds(w + wk + w_off[i], to + T::A_BYTES + min(wave * T::LW + i, T::NW - 1) * 1024);
+    };
+    auto clear_stage = [&](int k, uint8_t* stage) __attribute__((always_inline)) {
+        for (int i = threadIdx.x; i < (T::A_BYTES + T::W_BYTES) / 16; i += THREADS) {
+            const bool of_a = i < T::A_BYTES / 16;
+            const int at = of_a ? i : i - T::A_BYTES / 16, row = at / (of_a ? T::RA / 16 : T::RW / 16);
+            const int piece = of_a ? piece_of<T::RA>(row, at % (T::RA / 16)) : piece_of<T::RW>(row, at % (T::RW / 16));
+            if ((of_a ? k / (WIDE ? 1 : 2) : k / 2) + piece * 16 >= (of_a ? ab : wb))
+                reinterpret_cast<u4*>(stage)[i] = u4{0u, 0u, 0u, 0u};
+        }
     };
     // Scales of 512 elements of every row, rows of a first: by direct loads where every row's are 16-byte aligned (ALIGNED),
     // else through registers, and put_scales waits for all loads.
@@ -409,8 +436,17 @@ __global__ __launch_bounds__(WAVE * WM * WN, 2) void k_mx_many(ProductArgs p) {
             if constexpr (ALIGNED) {
                 // (a last piece of fewer rows than lanes writes past them, into what SCALES holds for it)
                 load_to_lds(row_scales(r, k), to + r0 * 16);
-            } else {
+            } else if (k + LONG <= p.k) {
                 __builtin_memcpy(&sc[i], row_scales(r, k), 16);
+            } else {
+                const uint8_t* from = row_scales(r, k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sc[i][e] = 0x7f7f7f7fu;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (k + (4 * e + c) * 32 < p.k) sc[i][e] = (sc[i][e] & ~(255u << (8 * c))) | (unsigned)from[4 * e + c] << (8 * c);
+                }
             }
         }
     };
@@ -464,8 +500,8 @@ __global__ __launch_bounds__(WAVE * WM * WN, 2) void k_mx_many(ProductArgs p) {
 
     // Stage i is multiplied while the RING - 1 stages after it come in.  The loads have one place in the loop, and the buffers
     // are told apart there: else the compiler would wait for all of them before it reads any.
-    const int whole = p.k / LONG, each = (whole + p.splits - 1) / p.splits, first = min((int)blockIdx.y * each, whole);
-    const int stages = (min(first + each, whole) - first) * (LONG / KS);
+    const int longs = (p.k + LONG - 1) / LONG, each = (longs + p.splits - 1) / p.splits, first = min((int)blockIdx.y * each, longs);
+    const int stages = (min(min(first + each, longs) * LONG, p.k) - min(first * LONG, p.k) + KS - 1) / KS;
     constexpr int PER = LONG / KS, LOADS = T::LA + T::LW;
     static_assert(RING - 2 <= PER, "scales are older than the loads that a wait leaves out");
     // (scales of the next 512 elements come into the other half of their buffer, which nothing reads at that time)
@@ -477,6 +513,10 @@ __global__ __launch_bounds__(WAVE * WM * WN, 2) void k_mx_many(ProductArgs p) {
             else
                 wait_loads<0>();
             __syncthreads();                       // stage i is there, and every wave is done with the buffer of stage i - 1
+            if (!ALIGNED && first * LONG + (i + 1) * KS > p.k) {
+                clear_stage(first * LONG + i * KS, const_cast<uint8_t*>(cur));
+                __syncthreads();
+            }
         }
         const int at = i + RING - 1, half = i / PER & 1, part = i % PER, more = i < 0 ? i + RING - 1 : i + PER;
         const bool fetch = (i < 0 ? i == 1 - RING : part == 0) && more < stages;
@@ -495,38 +535,54 @@ __global__ __launch_bounds__(WAVE * WM * WN, 2) void k_mx_many(ProductArgs p) {
         next = next == (RING - 1) * T::STAGE ? 0 : next + T::STAGE;
         if (i >= 0) cur = cur == (RING - 1) * T::STAGE ? 0 : cur + T::STAGE;
     }
-    if (whole * LONG < p.k && blockIdx.y == gridDim.y - 1) {
-        unsigned w_row[NT], a_row[MT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) w_row[j] = min(wn + 16 * j + lane % 16, p.n - 1 - n0);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) a_row[i] = min(wm + 16 * i + lane % 16, p.m - 1 - m0);
-        tail_steps<MODE, MT, NT>(p, w, ws, a, as, w_row, a_row, g, sum);
-    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(sum[i][j]));
+    const bool direct = p.splits > 1 ? p.n % 4 == 0 : p.vec;
+    float* part = p.splits > 1 ? p.part + (int64_t)blockIdx.y * p.m * p.n : nullptr;
+    if (direct) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = m0 + wm + 16 * i + lane % 16;
-        if (row >= p.m) continue;
+        for (int i = 0; i < MT; ++i) {
+            const int row = m0 + wm + 16 * i + lane % 16;
+            if (row >= p.m) continue;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int col = n0 + wn + 16 * j + 4 * g;
-            if (p.splits > 1) {
-                float* part = p.part + ((int64_t)blockIdx.y * p.m + row) * p.n + col;
-                if (p.n % 4 == 0) {
-                    if (col < p.n) *reinterpret_cast<f4*>(part) = sum[i][j];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < p.n) part[e] = sum[i][j][e];
-                }
-            } else if (col < p.n) {
-                store_out4<DT>(p, row, col, sum[i][j]);
+            for (int j = 0; j < NT; ++j) {
+                const int col = n0 + wn + 16 * j + 4 * g;
+                if (col >= p.n) continue;
+                if (part)
+                    *reinterpret_cast<f4*>(part + (int64_t)row * p.n + col) = sum[i][j];
+                else
+                    store_out4<DT>(p, row, col, sum[i][j]);
             }
         }
+        return;
+    }
+    // Outputs whose rows are not aligned go through LDS, so that a store takes a run of a row (3952 x 6755 x 224, float32: 91
+    // us with the four outputs of a lane one by one).
+    constexpr int ROW = NT * 16 + 4;
+    static_assert(T::WAVES * 16 * ROW * 4 <= T::LDS, "a piece of every wave");
+    float* mine = reinterpret_cast<float*>(smem) + wave * 16 * ROW;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int k = 0; k < MT; ++k)
+            if (k == i) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) *reinterpret_cast<f4*>(mine + r16 * ROW + 16 * j + 4 * g) = sum[k][j];
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");    // (written and read by this wave alone)
+        for (int e = lane; e < 16 * NT * 16; e += WAVE) {
+            const int row = m0 + wm + 16 * i + e / (NT * 16), col = n0 + wn + e % (NT * 16);
+            const float v = mine[e / (NT * 16) * ROW + e % (NT * 16)];
+            if (row >= p.m || col >= p.n) continue;
+            if (part)
+                part[(int64_t)row * p.n + col] = v;
+            else
+                store_out<DT>(p, row, col, v);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 

@@ -13,7 +13,13 @@ using namespace pi;
 
 namespace {
 
-constexpr int ST = 1024;                 // threads of a row's workgroup
+constexpr int ST = 512;                  // threads of a workgroup
+constexpr int EACH = 8;                  // logits of a thread and step
+constexpr int BINS = 2048;               // of a row's histogram
+constexpr int LIST = 4096;               // tokens in the bins that a rule's border lies in
+constexpr int MOST_CHUNKS = 256;         // of a row: 2^20 logits in chunks of 4096
+
+typedef unsigned long long u64;
 constexpr int FRACTION = 43;             // weights are integers of 2^-43: 2^20 of them sum below 2^63
 
 struct SampleArgs {
@@ -28,7 +34,27 @@ struct SampleArgs {
     float* prob;
     int* kept;
     int rows, vocab;
+    int chunks, chunk;                   // of a row; logits of one (a multiple of ST * EACH)
+    uint8_t* ws;
+    int64_t row_bytes;                   // of ws
 };
+
+// What the workgroups of a row leave for each other (offsets in the row's part of the workspace).
+struct Top {
+    unsigned most, least;                // largest and smallest key of a chunk (0: none)
+    int at, count;                       // lowest index of the largest; tokens that may be kept
+};
+struct RowState {
+    unsigned listed, done;               // tokens in the list, workgroups that have finished
+};
+constexpr int64_t WS_STATE = 0;
+constexpr int64_t WS_TOPS = 256;                                   // Top [chunks]
+constexpr int64_t WS_MASS = WS_TOPS + MOST_CHUNKS * 16;            // u64 [BINS]
+constexpr int64_t WS_COUNT = WS_MASS + BINS * 8;                   // unsigned [BINS]
+constexpr int64_t WS_CHUNK_MASS = WS_COUNT + BINS * 4;             // u64 [chunks]
+constexpr int64_t WS_CHUNK_KEPT = WS_CHUNK_MASS + MOST_CHUNKS * 8; // unsigned [chunks]
+constexpr int64_t WS_LIST = WS_CHUNK_KEPT + MOST_CHUNKS * 4;       // u64 [LIST]: key above the index's complement
+constexpr int64_t WS_ROW = WS_LIST + LIST * 8;
 
 // A logit as an unsigned integer in the same order; 0 for -inf and NaN, which are never kept.  -0 and 0 are equal.
 __device__ __forceinline__ unsigned order_key(float l) {
@@ -92,43 +118,14 @@ __device__ T before_and_total(T v, T* lds, T& total) {
     return base + incl - v;
 }
 
-// One workgroup per row.  The border of the kept set, in the order of the keys, is found digit by digit (8 bits, from
-// the top): top-k by counts, top-p by sums of weights.
+// A row by one workgroup, whatever it holds: the border of the kept set, in the order of the keys, is found digit by digit (8
+// bits, from the top), top-k by counts, top-p by sums of weights.  mass has room for 256.
 template <int DT>
-__global__ __launch_bounds__(ST) void k_sample(SampleArgs a) {
-    typedef unsigned long long u64;
-    __shared__ u64 mass[256];
-    __shared__ int count[256];
-    __shared__ u64 scan[ST / WAVE];
-    __shared__ unsigned best;
-    __shared__ int first;
+__device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* mass, u64* scan) {
     __shared__ unsigned s_key;
     __shared__ u64 s_before;
-    const int row = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x;
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
-    Rule rule = rule_of(a, row);
-
-    if (tid == 0) best = 0, first = a.vocab;
-    __syncthreads();
-    unsigned mine = 0;
-    int at = a.vocab;
-    for (int i = tid; i < a.vocab; i += ST) {
-        const unsigned key = order_key(logit<DT>(l, i));
-        if (key > mine) mine = key, at = i;
-    }
-    atomicMax(&best, mine);
-    __syncthreads();
-    if (mine == best && mine) atomicMin(&first, at);
-    __syncthreads();
-    if (best == 0 || rule.greedy) {
-        if (tid == 0) {
-            a.token[row] = best ? first : -1;
-            if (a.prob) a.prob[row] = best ? 1.0f : 0.0f;
-            if (a.kept) a.kept[row] = best ? 1 : 0;
-        }
-        return;
-    }
-    rule.top = key_logit(best);
 
     // kept: keys above `key`, and of those equal to it the first `ties` by index
     unsigned key = 1;
@@ -142,7 +139,7 @@ __global__ __launch_bounds__(ST) void k_sample(SampleArgs a) {
         const unsigned floor_key = key;
         const int64_t floor_ties = ties;
         for (int shift = 24; shift >= 0 && !all; shift -= 8) {
-            for (int b = tid; b < 256; b += ST) mass[b] = 0, count[b] = 0;
+            for (int b = tid; b < 256; b += ST) mass[b] = 0;
             __syncthreads();
             for (int i = tid; i < a.vocab; i += ST) {
                 const float x = logit<DT>(l, i);
@@ -228,7 +225,465 @@ __global__ __launch_bounds__(ST) void k_sample(SampleArgs a) {
     }
 }
 
-size_t sample_bytes(int, int) { return 256; }
+// ---- a row by many workgroups --------------------------------------------------------
+//
+// The logits' bytes would take a microsecond or two; what there is to do is to keep a row's pieces busy at the same time,
+// and to read them few times.  Three launches, a workgroup to each chunk of a row:
+//   k_sample_top     the largest and smallest logit of the chunk
+//   k_sample_count   with the row's largest known: the chunk's part of a histogram of the distance to it (counts for top-k,
+//                    sums of weights for top-p); without either rule the sum of its weights
+//   k_sample_pick    from the histogram the bins in which the border of top-k and of top-p can lie: sums over the tokens
+//                    above them, and a list of the tokens in them; the row's last workgroup sorts the list, finds the border and
+//                    the token
+// Sums are integers, so that neither their order nor that of the list matters.  A row whose border bins hold more than
+// LIST tokens (equal logits, or a border far below the others) is done by its last workgroup alone, from the start.
+
+// 8 logits from i on; those past the row's end are -inf
+template <int DT>
+__device__ __forceinline__ void load_logits(const uint8_t* row, int i, int vocab, float* v) {
+    if (i + EACH <= vocab) {
+        if constexpr (DT == F16) {
+            h8 t;
+            __builtin_memcpy(&t, row + (int64_t)i * 2, 16);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) v[e] = (float)t[e];
+        } else {
+            f4 t[2];
+            __builtin_memcpy(t, row + (int64_t)i * 4, 32);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) v[e] = t[e / 4][e % 4];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) v[e] = i + e < vocab ? logit<DT>(row, i + e) : -INFINITY;
+    }
+}
+
+__device__ __forceinline__ unsigned wave_max(unsigned v) {
+#pragma unroll
+    for (int o = 1; o < WAVE; o *= 2) v = max(v, (unsigned)__shfl_xor((int)v, o));
+    return v;
+}
+__device__ __forceinline__ u64 wave_sum(u64 v) {
+#pragma unroll
+    for (int o = 1; o < WAVE; o *= 2) v += __shfl_xor(v, o);
+    return v;
+}
+
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
+    __shared__ unsigned s_most[ST / WAVE], s_least[ST / WAVE], s_at[ST / WAVE];
+    __shared__ int s_count[ST / WAVE];
+    const int row = blockIdx.y, tid = threadIdx.x, wave = tid / WAVE;
+    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
+    uint8_t* ws = a.ws + row * a.row_bytes;
+    // what the later launches add to
+    for (int b = blockIdx.x * ST + tid; b < BINS; b += gridDim.x * ST) {
+        reinterpret_cast<u64*>(ws + WS_MASS)[b] = 0;
+        reinterpret_cast<unsigned*>(ws + WS_COUNT)[b] = 0;
+    }
+    if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<RowState*>(ws + WS_STATE) = RowState{0u, 0u};
+
+    // the smallest key as the largest of the complements
+    unsigned most = 0, low = 0, at = 0;
+    int count = 0;
+    const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
+    for (int i = from + tid * EACH; i < to; i += ST * EACH) {
+        float v[EACH];
+        load_logits<DT>(l, i, a.vocab, v);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const unsigned key = order_key(v[e]);
+            if (key > most) most = key, at = i + e;
+            low = max(low, key ? ~key : 0u);
+            count += key != 0;
+        }
+    }
+    const unsigned top = wave_max(most);
+    // the lowest index of the largest (a thread has met its own lowest first)
+    const unsigned first = ~wave_max(most == top ? ~at : 0u);
+    low = wave_max(low);
+    count = (int)wave_sum((u64)count);
+    if (tid % WAVE == 0) s_most[wave] = top, s_at[wave] = first, s_least[wave] = low, s_count[wave] = count;
+    __syncthreads();
+    if (tid) return;
+    Top t{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < ST / WAVE; ++w) {
+        if (s_most[w] > t.most || (s_most[w] == t.most && (int)s_at[w] < t.at)) t.most = s_most[w], t.at = (int)s_at[w];
+        t.least = max(t.least, s_least[w]);
+        t.count += s_count[w];
+    }
+    t.least = ~t.least;
+    reinterpret_cast<Top*>(ws + WS_TOPS)[blockIdx.x] = t;
+}
+
+// The row's largest and smallest key, the largest's lowest index, and the tokens that may be kept, from its chunks'.
+__device__ __forceinline__ Top row_top(const SampleArgs& a, const uint8_t* ws, Top* s_top) {
+    if (threadIdx.x < WAVE) {
+        Top t{0, ~0u, 0, 0};
+        for (int c = threadIdx.x; c < a.chunks; c += WAVE) {
+            const Top o = reinterpret_cast<const Top*>(ws + WS_TOPS)[c];
+            if (o.most > t.most) t.most = o.most, t.at = o.at;
+            t.least = min(t.least, o.least);
+            t.count += o.count;
+        }
+        const unsigned top = wave_max(t.most);
+        t.at = (int)~wave_max(t.most == top ? ~(unsigned)t.at : 0u);
+        t.least = ~wave_max(~t.least);
+        t.count = (int)wave_sum((u64)t.count);
+        t.most = top;
+        if (threadIdx.x == 0) *s_top = t;
+    }
+    __syncthreads();
+    return *s_top;
+}
+
+// Bin of a logit: its distance to the largest, in steps that cover the tokens with a weight (40 temperatures) or, for top-k,
+// at least 64; everything farther in the last one.
+struct Binning {
+    float top, scale;
+    __device__ Binning(const Rule& r, const Top& t) : top(r.top) {
+        const float range = top - key_logit(t.least), span = (float)(40.0 / r.inv_t);
+        const float most = fminf(fminf(range, r.top_k ? fmaxf(span, 64.0f) : span), 3e38f);
+        scale = most > 0.0f ? (float)(BINS - 1) / most : 0.0f;
+        if (!(scale < INFINITY)) scale = 3e38f;
+    }
+    __device__ __forceinline__ int of(float l) const {
+        if (l == top) return 0;
+        return (int)fminf((top - l) * scale, (float)(BINS - 1));
+    }
+};
+
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
+    __shared__ u64 s_mass[BINS];
+    __shared__ unsigned s_count[BINS];
+    __shared__ Top s_top;
+    __shared__ u64 s_sum;
+    const int row = blockIdx.y, tid = threadIdx.x;
+    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
+    uint8_t* ws = a.ws + row * a.row_bytes;
+    Rule rule = rule_of(a, row);
+    const Top t = row_top(a, ws, &s_top);
+    if (t.most == 0 || rule.greedy) return;
+    rule.top = key_logit(t.most);
+    if (rule.top_k >= t.count) rule.top_k = 0;
+    const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
+    const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
+    if (!by_count && !by_mass) {
+        u64 sum = 0;
+        unsigned n = 0;
+        for (int i = from + tid * EACH; i < to; i += ST * EACH) {
+            float v[EACH];
+            load_logits<DT>(l, i, a.vocab, v);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) {
+                if (!order_key(v[e])) continue;
+                const double w = rule.weight(v[e]);
+                if (w >= rule.min_p) sum += fixed(w), ++n;
+            }
+        }
+        if (tid == 0) s_sum = 0, s_count[0] = 0;
+        __syncthreads();
+        sum = wave_sum(sum);
+        n = (unsigned)wave_sum((u64)n);
+        if (tid % WAVE == 0) atomicAdd(&s_sum, sum), atomicAdd(&s_count[0], n);
+        __syncthreads();
+        if (tid == 0) {
+            reinterpret_cast<u64*>(ws + WS_CHUNK_MASS)[blockIdx.x] = s_sum;
+            reinterpret_cast<unsigned*>(ws + WS_CHUNK_KEPT)[blockIdx.x] = s_count[0];
+        }
+        return;
+    }
+    const Binning bin(rule, t);
+    for (int b = tid; b < BINS; b += ST) s_mass[b] = 0, s_count[b] = 0;
+    __syncthreads();
+    for (int i = from + tid * EACH; i < to; i += ST * EACH) {
+        float v[EACH];
+        load_logits<DT>(l, i, a.vocab, v);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            if (!order_key(v[e])) continue;
+            const int b = bin.of(v[e]);
+            atomicAdd(&s_count[b], 1u);
+            if (by_mass) {
+                const u64 w = fixed(rule.weight(v[e]));
+                if (w) atomicAdd(&s_mass[b], w);
+            }
+        }
+    }
+    __syncthreads();
+    for (int b = tid; b < BINS; b += ST) {
+        if (!s_count[b]) continue;
+        atomicAdd(reinterpret_cast<unsigned*>(ws + WS_COUNT) + b, s_count[b]);
+        if (s_mass[b]) atomicAdd(reinterpret_cast<u64*>(ws + WS_MASS) + b, s_mass[b]);
+    }
+}
+
+// the lowest bin with which the running sum reaches `want`; BINS if none does.  before: the sum of this thread's bins'
+// predecessors; own: its BINS / ST bins' values
+__device__ __forceinline__ void find_bin(u64 want, u64 before, const u64* own, int* s_bin) {
+    u64 sum = before;
+#pragma unroll
+    for (int e = 0; e < BINS / ST; ++e) {
+        if (sum < want && sum + own[e] >= want) *s_bin = threadIdx.x * (BINS / ST) + e;
+        sum += own[e];
+    }
+}
+
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
+    __shared__ u64 s_list[LIST];
+    __shared__ u64 scan[ST / WAVE];
+    __shared__ u64 s_mass[MOST_CHUNKS];
+    __shared__ unsigned s_kept[MOST_CHUNKS];
+    __shared__ Top s_top;
+    __shared__ int s_bin[3];
+    __shared__ u64 s_at[5];
+    __shared__ u64 s_sum;
+    __shared__ unsigned s_n, s_last;
+    const int row = blockIdx.y, tid = threadIdx.x;
+    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
+    uint8_t* ws = a.ws + row * a.row_bytes;
+    RowState* state = reinterpret_cast<RowState*>(ws + WS_STATE);
+    Rule rule = rule_of(a, row);
+    const Top t = row_top(a, ws, &s_top);
+    if (t.most == 0 || rule.greedy) {
+        if (blockIdx.x == 0 && tid == 0) {
+            a.token[row] = t.most ? t.at : -1;
+            if (a.prob) a.prob[row] = t.most ? 1.0f : 0.0f;
+            if (a.kept) a.kept[row] = t.most ? 1 : 0;
+        }
+        return;
+    }
+    rule.top = key_logit(t.most);
+    if (rule.top_k >= t.count) rule.top_k = 0;
+    const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
+    const Binning bin(rule, t);
+
+    // Bins: k_bin holds the border of top-k; the sum that top-p is a part of lies between those without and with it, so the
+    // border of top-p lies in p_lo .. p_hi.
+    int k_bin = BINS, p_lo = BINS, p_hi = BINS;
+    u64 k_before = 0, mass_lo = 0, p_before = 0;      // tokens before k_bin, weights before it and before p_lo
+    if (by_count || by_mass) {
+        u64 n[BINS / ST], m[BINS / ST], own_n = 0, own_m = 0, all_n, all_m;
+#pragma unroll
+        for (int e = 0; e < BINS / ST; ++e) {
+            n[e] = reinterpret_cast<const unsigned*>(ws + WS_COUNT)[tid * (BINS / ST) + e];
+            m[e] = reinterpret_cast<const u64*>(ws + WS_MASS)[tid * (BINS / ST) + e];
+            own_n += n[e], own_m += m[e];
+        }
+        const u64 before_n = before_and_total<u64>(own_n, scan, all_n), before_m = before_and_total<u64>(own_m, scan, all_m);
+        if (tid < 3) s_bin[tid] = BINS;
+        __syncthreads();
+        if (by_count) find_bin((u64)rule.top_k, before_n, n, &s_bin[0]);
+        __syncthreads();
+        k_bin = s_bin[0];
+        if (tid == 0) s_at[0] = s_at[2] = 0, s_at[1] = s_at[3] = all_m;
+        __syncthreads();
+        if (k_bin < BINS && k_bin / (BINS / ST) == tid) {
+            u64 c = before_n, w = before_m;
+            for (int e = 0; e < k_bin % (BINS / ST); ++e) c += n[e], w += m[e];
+            s_at[0] = c, s_at[1] = w, s_at[3] = w + m[k_bin % (BINS / ST)];
+        }
+        __syncthreads();
+        k_before = s_at[0], mass_lo = s_at[1];
+        if (by_mass) {
+            const double lo = ceil(rule.top_p * (double)mass_lo), hi = ceil(rule.top_p * (double)s_at[3]);
+            find_bin(lo > 1.0 ? (u64)lo : 1, before_m, m, &s_bin[1]);
+            find_bin(hi > 1.0 ? (u64)hi : 1, before_m, m, &s_bin[2]);
+            __syncthreads();
+            p_lo = s_bin[1], p_hi = s_bin[2];
+            if (p_lo < BINS && p_lo / (BINS / ST) == tid) {
+                u64 w = before_m;
+                for (int e = 0; e < p_lo % (BINS / ST); ++e) w += m[e];
+                s_at[2] = w;
+            }
+            __syncthreads();
+            p_before = s_at[2];
+        }
+    }
+    const int border = by_mass ? p_lo : k_bin;           // bins before it are kept for certain
+
+    if (by_count || by_mass) {
+        if (tid == 0) s_sum = 0, s_n = 0;
+        __syncthreads();
+        u64 sum = 0;
+        unsigned n = 0;
+        const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
+        for (int i = from + tid * EACH; i < to; i += ST * EACH) {
+            float v[EACH];
+            load_logits<DT>(l, i, a.vocab, v);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) {
+                const unsigned key = order_key(v[e]);
+                if (!key) continue;
+                const int b = bin.of(v[e]);
+                if (b < border) {
+                    const double w = rule.weight(v[e]);
+                    if (w >= rule.min_p) sum += fixed(w), ++n;
+                } else if (b == k_bin || (by_mass && b <= p_hi)) {
+                    const unsigned at = atomicAdd(&state->listed, 1u);
+                    if (at < LIST) reinterpret_cast<u64*>(ws + WS_LIST)[at] = (u64)key << 32 | ~(unsigned)(i + e);
+                }
+            }
+        }
+        sum = wave_sum(sum);
+        n = (unsigned)wave_sum((u64)n);
+        if (tid % WAVE == 0 && n) atomicAdd(&s_sum, sum), atomicAdd(&s_n, n);
+        __syncthreads();
+        if (tid == 0) {
+            reinterpret_cast<u64*>(ws + WS_CHUNK_MASS)[blockIdx.x] = s_sum;
+            reinterpret_cast<unsigned*>(ws + WS_CHUNK_KEPT)[blockIdx.x] = s_n;
+        }
+    }
+
+    // the row's last workgroup goes on
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(&state->done, 1u) == (unsigned)a.chunks - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const unsigned listed = __hip_atomic_load(&state->listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (listed > LIST) {
+        whole_row<DT>(a, row, rule, s_list, scan);
+        return;
+    }
+    for (int c = tid; c < a.chunks; c += ST) {
+        s_mass[c] = __hip_atomic_load(reinterpret_cast<u64*>(ws + WS_CHUNK_MASS) + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_kept[c] = __hip_atomic_load(reinterpret_cast<unsigned*>(ws + WS_CHUNK_KEPT) + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // the list, largest first
+    int size = WAVE;
+    while (size < (int)listed) size *= 2;
+    for (int i = tid; i < size; i += ST)
+        s_list[i] = i < (int)listed
+                        ? __hip_atomic_load(reinterpret_cast<u64*>(ws + WS_LIST) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                        : 0ull;
+    __syncthreads();
+    for (int run = 2; listed > 1 && run <= size; run *= 2)
+        for (int step = run / 2; step > 0; step /= 2) {
+            for (int i = tid; i < size / 2; i += ST) {
+                const int x = 2 * i - (i & (step - 1)), y = x + step;
+                const u64 p = s_list[x], q = s_list[y];
+                if ((p < q) == ((x & run) == 0)) s_list[x] = q, s_list[y] = p;
+            }
+            __syncthreads();
+        }
+
+    // How many of the list are kept: a prefix.  Its tokens of k_bin are the last; top-k keeps top_k - k_before of them.
+    unsigned last_key = 1, last_at = 0xffffffffu;        // the last token kept
+    if (listed) {
+        constexpr int PER = LIST / ST;
+        u64 w[PER], own = 0, own_k = 0, all, in_k;
+        int of_k = 0;
+        const int per = (size + ST - 1) / ST;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int i = tid * per + e;
+            w[e] = 0;
+            if (e < per && i < (int)listed) {
+                const float x = key_logit((unsigned)(s_list[i] >> 32));
+                w[e] = fixed(rule.weight(x));
+                of_k += by_count && bin.of(x) == k_bin;
+            }
+        }
+        // tokens of the list before those of k_bin, and how many of the list top-k leaves
+        u64 n_k;
+        before_and_total<u64>((u64)of_k, scan, n_k);
+        const int begin_k = (int)listed - (int)n_k;
+        const int by_k = by_count ? begin_k + (int)((u64)rule.top_k - k_before) : (int)listed;
+        int keep = by_k;
+        if (by_mass) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid * per + e;
+                if (e >= per || i >= by_k) w[e] = 0;
+                own += w[e];
+                if (i >= begin_k) own_k += w[e];
+            }
+            before_and_total<u64>(own_k, scan, in_k);
+            const u64 before = p_before + before_and_total<u64>(own, scan, all);
+            const double p = ceil(rule.top_p * (double)(mass_lo + in_k));
+            const u64 want = p > 1.0 ? (u64)p : 1;
+            // (past p_hi there are tokens that the list leaves out, but the sum has reached `want` before)
+            u64 run = before;
+            int n = 0;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid * per + e;
+                if (e < per && i < by_k && run < want) ++n;
+                run += w[e];
+            }
+            u64 total_n;
+            before_and_total<u64>((u64)n, scan, total_n);
+            keep = (int)total_n;
+        }
+        const u64 last = s_list[max(keep, 1) - 1];
+        last_key = (unsigned)(last >> 32), last_at = ~(unsigned)last;
+        for (int i = tid; i < keep; i += ST) {
+            const double x = rule.weight(key_logit((unsigned)(s_list[i] >> 32)));
+            const int c = (int)(~(unsigned)s_list[i]) / a.chunk;
+            if (x >= rule.min_p) atomicAdd(&s_mass[c], fixed(x)), atomicAdd(&s_kept[c], 1u);
+        }
+        __syncthreads();
+    } else {
+        __syncthreads();
+    }
+
+    // the chunk that the random number falls into
+    u64 total, kept;
+    const u64 mine = tid < a.chunks ? s_mass[tid] : 0;
+    const u64 before = before_and_total<u64>(mine, scan, total);
+    before_and_total<u64>(tid < a.chunks ? (u64)s_kept[tid] : 0ull, scan, kept);
+    const float u = a.u[row];
+    u64 target = u > 0.0f ? (u64)((double)u * (double)total) : 0;
+    if (u >= 1.0f || target >= total) target = total - 1;
+    if (tid == 0 && a.kept) a.kept[row] = (int)kept;
+    if (before <= target && target < before + mine) s_n = tid, s_sum = before;
+    __syncthreads();
+    // and the token in it: every thread a run
+    const int run = a.chunk / ST, from = (int)s_n * a.chunk + tid * run, to = min(from + run, a.vocab);
+    auto weight = [&](int i) __attribute__((always_inline)) {
+        const float x = logit<DT>(l, i);
+        const unsigned key = order_key(x);
+        if (key < last_key || (key == last_key && (unsigned)i > last_at)) return 0ull;
+        const double w = rule.weight(x);
+        return w >= rule.min_p ? (u64)fixed(w) : 0ull;
+    };
+    u64 sum = 0, in_chunk;
+    for (int i = from; i < to; ++i) sum += weight(i);
+    u64 at = s_sum + before_and_total<u64>(sum, scan, in_chunk);
+    if (target < at || target >= at + sum) return;
+    for (int i = from; i < to; ++i) {
+        const u64 w = weight(i);
+        at += w;
+        if (at > target) {
+            a.token[row] = i;
+            if (a.prob) a.prob[row] = (float)((double)w / (double)total);
+            return;
+        }
+    }
+}
+
+size_t sample_bytes(int rows, int) { return (size_t)rows * WS_ROW; }
+
+// Chunks of a row so that some 512 workgroups have work, of 4096 logits at least (eight for a thread).
+void chunks_of(SampleArgs& a) {
+    const int step = ST * EACH, want = std::max(1, 512 / a.rows);
+    a.chunk = std::max(1, (int)(((int64_t)a.vocab + (int64_t)want * step - 1) / ((int64_t)want * step))) * step;
+    a.chunks = (a.vocab + a.chunk - 1) / a.chunk;
+}
+
+template <int DT>
+pi_status sample(const SampleArgs& a, hipStream_t s) {
+    const dim3 grid(a.chunks, a.rows), block(ST);
+    TRY(launch(PI_K_SAMPLE, k_sample_top<DT>, grid, block, 0, s, a));
+    TRY(launch(PI_K_SAMPLE, k_sample_count<DT>, grid, block, 0, s, a));
+    return launch(PI_K_SAMPLE, k_sample_pick<DT>, grid, block, 0, s, a);
+}
 
 }  // namespace
 
@@ -257,10 +712,9 @@ pi_status pi_sample(const void* logits, int32_t rows, int32_t vocab, int64_t row
           sample_bytes(rows, vocab));
     CHECK(aligned(ws, 256), PI_ERR_ALIGN, "sample: workspace must be 256-byte aligned");
     SampleArgs a{(const uint8_t*)logits, row_stride, rule->temperature, rule->top_k, rule->top_p, rule->min_p, u, token, prob,
-                 kept, rows, vocab};
-    hipStream_t s = (hipStream_t)stream;
-    return dtype == PI_F16 ? launch(PI_K_SAMPLE, k_sample<F16>, dim3(rows), dim3(ST), 0, s, a)
-                           : launch(PI_K_SAMPLE, k_sample<F32>, dim3(rows), dim3(ST), 0, s, a);
+                 kept, rows, vocab, 0, 0, (uint8_t*)ws, WS_ROW};
+    chunks_of(a);
+    return dtype == PI_F16 ? sample<F16>(a, (hipStream_t)stream) : sample<F32>(a, (hipStream_t)stream);
 }
 
 }  // extern "C"

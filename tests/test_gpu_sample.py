@@ -161,6 +161,48 @@ def test_top_k_below_the_weights_that_count():
     check(l, [0.1, 0.6, 0.99], k=[4000, 7000, 9000])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_borders_in_long_rows(dtype):
+    """Rows of many chunks whose borders lie where many tokens are: top-k and top-p far down, alone and together, ties at them."""
+    rng = np.random.default_rng(12)
+    l = rows_of(rng, 8, 70001, dtype, 1.0)
+    l[6:] = np.round(l[6:] * 4) / 4                               # a few values, thousands of tokens each
+    u = rng.random(8).astype(np.float32)
+    k = np.array([1, 2, 5000, 30000, 69000, 70001, 20000, 60000], np.int32)
+    p = np.array([0.0103, 0.3007, 0.5003, 0.9007, 0.9993, 0.99993, 0.4003, 0.8507], np.float32)
+    t = np.array([0.2, 1, 3, 1, 0.7, 1, 1, 2], np.float32)
+    check(l, u, t, k=k)
+    check(l, u, t, p=p)
+    check(l, u, t, k=k, p=p)
+    check(l, u, t, k=k, p=p, m=np.full(8, 0.01, np.float32), pad=5, off=3)
+    check(l, u, t, k=np.full(8, 40, np.int32), p=p)
+
+
+def test_calls_on_two_streams_and_after_each_other():
+    """The same workspace for one call after another, others for calls at the same time: every call as it is alone."""
+    rng = np.random.default_rng(4)
+    l = [dev(rows_of(rng, n, v, "f32")) for n, v in ((3, 90001), (17, 5000))]
+    u = [dev(rng.random(x.shape[0]).astype(np.float32)) for x in l]
+    rule = [pb.make_sample_rule(top_k=torch.full((x.shape[0],), 40, dtype=torch.int32, device=DEV),
+                                top_p=torch.full((x.shape[0],), 0.9, device=DEV)) for x in l]
+    ws = [torch.full((pb.pi_sample_workspace_bytes(*x.shape),), 255, dtype=torch.uint8, device=DEV) for x in l]
+    alone = []
+    for x, r, n, w in zip(l, rule, u, ws):
+        token, prob = torch.empty(x.shape[0], dtype=torch.int32, device=DEV), torch.empty(x.shape[0], device=DEV)
+        pb.pi_sample(x, r, n, token, prob, None, w)
+        torch.cuda.synchronize()
+        alone.append((token.clone(), prob.clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[(torch.empty_like(t), torch.empty_like(p)) for _ in range(10)] for t, p in alone]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for x, r, n, w, s, o in zip(l, rule, u, ws, streams, outs):
+            pb.pi_sample(x, r, n, o[i][0], o[i][1], None, w, stream=s)
+    torch.cuda.synchronize()
+    for (t, p), o in zip(alone, outs):
+        assert all(torch.equal(a, t) and torch.equal(b, p) for a, b in o)
+
+
 def test_draws_follow_the_distribution():
     """20000 rows of one distribution, evenly spaced numbers: each token as often as its weight says, within one row."""
     l = np.array([[0.0, 1.0, -np.inf, 2.0, 1.5, -1.0]], np.float32)
