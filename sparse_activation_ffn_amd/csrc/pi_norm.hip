@@ -60,12 +60,16 @@ __device__ __forceinline__ double lanes_sum(double v) {
     return v;
 }
 
-// the sum over the whole workgroup
+// the sum over a workgroup of N threads
+template <int N>
 __device__ __forceinline__ double workgroup_sum(double v, double* lds) {
     v = lanes_sum<64>(v);
     if (threadIdx.x % WAVE == 0) lds[threadIdx.x / WAVE] = v;
     __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    double sum = lds[0];
+#pragma unroll
+    for (int i = 1; i < N / WAVE; ++i) sum += lds[i];
+    return sum;
 }
 
 template <int XT>
@@ -77,43 +81,67 @@ __device__ __forceinline__ float element(const uint8_t* p, int dtype, int i) {
     return dtype == F16 ? (float)reinterpret_cast<const _Float16*>(p)[i] : reinterpret_cast<const float*>(p)[i];
 }
 
-// The float32 next to a value, y its nearest and rest = value - y, whose last bit is 1 unless the value is y: rounded on
-// to fewer bits, it gives what the value itself would.
-__device__ __forceinline__ float to_odd(float y, float rest) {
-    unsigned b = __builtin_bit_cast(unsigned, y);
-    if (rest < 0.0f ? y > 0.0f : rest > 0.0f && y < 0.0f) --b;
-    return __builtin_bit_cast(float, b | (rest != 0.0f ? 1u : 0u));
-}
-
-// y of one element, as the nearest float32 and to odd.  f16 times f16 is exact in float32, so with r as a sum of two floats
-// one rounding is left, and its rest is known; the other forms go through 64 bits, which costs nothing at the HBM rate.
+// y of one element.  f16 times f16 is exact in float32, so with r as a sum of two floats one rounding is left; the other
+// forms go through 64 bits.  ODD: the float32 next to y whose last bit is 1, unless y is one: rounded on to fewer bits, it
+// gives what y itself would.  That costs twice the operations, so it is for values that may lie half between two codes,
+// where the nearest float32 has 19 bits of zeros at its end (which at this distance from y is one in 2^19).
 struct Scale {
     double r;
     float hi, lo;
-    __device__ explicit Scale(double mean_eps) : r(1.0 / sqrt(mean_eps)), hi((float)r), lo((float)(r - (double)hi)) {}
-    template <bool EXACT>
-    __device__ __forceinline__ float of(float s, float w, float& odd) const {
+    __device__ explicit Scale(double mean_eps) {
+        // the instruction's 24 bits or so, doubled twice
+        r = __builtin_amdgcn_rsq(mean_eps);
+        if (mean_eps > 0.0 && mean_eps < (double)INFINITY) {
+            r = r * fma(-0.5 * mean_eps * r, r, 1.5);
+            r = r * fma(-0.5 * mean_eps * r, r, 1.5);
+        }
+        hi = (float)r, lo = (float)(r - (double)hi);
+    }
+    template <bool EXACT, bool ODD>
+    __device__ __forceinline__ float of(float s, float w) const {
         float y, rest;
         if constexpr (EXACT) {
             const float t = s * w;
             const float low = fabsf(t) < INFINITY ? t * lo : 0.0f;   // (an infinite weight meets lo of either sign)
             y = fmaf(t, hi, low);
-            rest = fmaf(t, hi, -y) + low;
+            rest = ODD ? fmaf(t, hi, -y) + low : 0.0f;
         } else {
             const double v = (double)s * r * (double)w;
             y = (float)v;
-            rest = (float)(v - (double)y);
+            rest = ODD ? (float)(v - (double)y) : 0.0f;
         }
-        odd = to_odd(y, fabsf(y) < INFINITY ? rest : 0.0f);
+        if (ODD && fabsf(y) < INFINITY && rest != 0.0f) {
+            unsigned b = __builtin_bit_cast(unsigned, y);
+            if ((rest < 0.0f) == (y > 0.0f)) --b;
+            y = __builtin_bit_cast(float, b | 1u);
+        }
         return y;
     }
 };
 
-// TPR threads to a row, C chunks of 8 elements to a thread.  d % 8 == 0 and every row 16-byte aligned.
-template <int XT, int TPR, int C>
-__global__ __launch_bounds__(NT) void k_rms_norm(NormArgs a) {
-    constexpr int PER = NT / TPR;                        // rows of a workgroup
-    __shared__ double lds[NT / WAVE];
+__device__ __forceinline__ bool may_be_tie(float y) { return (__builtin_bit_cast(unsigned, y) & 0x7ffffu) == 0; }
+
+// 8 elements as they are stored: float32 takes two pieces of 16 bytes
+template <int DT>
+struct Raw8 {
+    u4 v[DT == F16 ? 1 : 2];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        v[0] = ld16(p);
+        if constexpr (DT == F32) v[1] = ld16(p + 16);
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (DT == F32) return bits_f(v[e / 4][e % 4]);
+        return e % 2 ? half_hi(v[0][e / 2]) : half_lo(v[0][e / 2]);
+    }
+    __device__ __forceinline__ void set(const float* f) { store8<DT, true>(v, f); }
+};
+
+// TPR threads to a row, C chunks of 8 elements to a thread, the sum kept as it is stored.  d % 8 == 0 and every row 16-byte
+// aligned.  FORMAT: of the microscaled output, or NONE.
+template <int XT, int TPR, int C, int FORMAT>
+__global__ __launch_bounds__(std::max(NT, TPR)) void k_rms_norm(NormArgs a) {
+    constexpr int PER = std::max(NT / TPR, 1);           // rows of a workgroup
+    __shared__ double lds[std::max(NT, TPR) / WAVE];
     const int t = threadIdx.x % TPR;
     const int row = blockIdx.x * PER + threadIdx.x / TPR;
     if (PER > 1 && row >= a.rows) return;                // (whole groups of lanes that work together)
@@ -121,51 +149,7 @@ __global__ __launch_bounds__(NT) void k_rms_norm(NormArgs a) {
     constexpr int ES = XT == F16 ? 2 : 4;
     const uint8_t* x = a.x + token * a.x_ts + head * a.x_hs;
     const uint8_t* delta = a.delta + token * a.d_ts + head * a.d_hs;
-    float s[C][8];
-    double squares = 0.0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int at = (c * TPR + t) * 8;
-        if (at < a.d) {
-            load8<XT, true>(x + (int64_t)at * ES, s[c]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[c][e] = 0.0f;
-        }
-    }
-    if (a.ddtype != NONE) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int at = (c * TPR + t) * 8;
-            if (at < a.d) {
-                float dv[8];
-                if (a.ddtype == F16)
-                    load8<F16, true>(delta + (int64_t)at * 2, dv);
-                else
-                    load8<F32, true>(delta + (int64_t)at * 4, dv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[c][e] = rounded<XT>(s[c][e] + dv[e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) squares = fma((double)s[c][e], (double)s[c][e], squares);
-    double total;
-    if constexpr (TPR <= WAVE)
-        total = lanes_sum<TPR>(squares);
-    else
-        total = workgroup_sum(squares, lds);
-    const Scale scale(total / a.d + a.eps);
-    uint8_t* sum = a.sum + token * a.s_ts + head * a.s_hs;
-    uint8_t* y = a.y + token * a.y_ts + head * a.y_hs;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int at = (c * TPR + t) * 8;
-        if (at >= a.d) continue;
-        if (a.sum) store8<XT, true>(sum + (int64_t)at * ES, s[c]);
-        float w[8], v[8], odd[8];
+    auto load_weight = [&](int at, float* w) __attribute__((always_inline)) {
         if (a.wdtype == F16)
             load8<F16, true>(a.weight + (int64_t)at * 2, w);
         else if (a.wdtype == F32)
@@ -173,19 +157,83 @@ __global__ __launch_bounds__(NT) void k_rms_norm(NormArgs a) {
         else
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-        if (XT == F16 && a.wdtype != F32) {
+    };
+    Raw8<XT> s[C];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = scale.of<true>(s[c][e], w[e], odd[e]);
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+        if (at < a.d)
+            s[c].load(x + (int64_t)at * ES);
+        else
+            s[c] = Raw8<XT>{};
+    }
+    // (asked for before the sum, which is a barrier away, where there are registers for it)
+    float w[8];
+    if (C == 1 && t * 8 < a.d) load_weight(t * 8, w);
+    if (a.ddtype != NONE) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = (c * TPR + t) * 8;
+            if (at < a.d) {
+                float v[8];
+                if (a.ddtype == F16)
+                    load8<F16, true>(delta + (int64_t)at * 2, v);
+                else
+                    load8<F32, true>(delta + (int64_t)at * 4, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += s[c].get(e);
+                s[c].set(v);
+            }
+        }
+    }
+    double squares = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) squares = fma((double)s[c].get(e), (double)s[c].get(e), squares);
+    double total;
+    if constexpr (TPR <= WAVE)
+        total = lanes_sum<TPR>(squares);
+    else
+        total = workgroup_sum<TPR>(squares, lds);
+    // (opaque, so that the elements are kept as they are stored and not as the float32 of the squares)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < (XT == F16 ? 1 : 2); ++i) asm volatile("" : "+v"(s[c].v[i]));
+    const Scale scale(total / a.d + a.eps);
+    uint8_t* sum = a.sum + token * a.s_ts + head * a.s_hs;
+    uint8_t* y = a.y + token * a.y_ts + head * a.y_hs;
+    const bool exact = XT == F16 && a.wdtype != F32;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+        if (at >= a.d) continue;
+        if (a.sum) {
+            reinterpret_cast<u4*>(sum + (int64_t)at * ES)[0] = s[c].v[0];
+            if constexpr (XT == F32) reinterpret_cast<u4*>(sum + (int64_t)at * ES)[1] = s[c].v[1];
+        }
+        if (C > 1) load_weight(at, w);
+        float v[8];
+        if (exact) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = scale.of<true, false>(s[c].get(e), w[e]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = scale.of<false>(s[c][e], w[e], odd[e]);
+            for (int e = 0; e < 8; ++e) v[e] = scale.of<false, false>(s[c].get(e), w[e]);
         }
-        if (a.y) store8<XT, true>(y + (int64_t)at * ES, XT == F16 ? odd : v);
-        const int64_t in_all = (int64_t)row * a.d + at;
-        if (a.format == PI_MXFP8)
-            store_block<PI_MXFP8>(odd, in_all, a.codes, a.scales);
-        else if (a.format == PI_MXFP4)
-            store_block<PI_MXFP4>(odd, in_all, a.codes, a.scales);
+        if (a.y) store8<XT, true>(y + (int64_t)at * ES, v);
+        if constexpr (FORMAT != NONE) {
+            bool tie = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) tie |= may_be_tie(v[e]);
+            if (__any(tie)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = exact ? scale.of<true, true>(s[c].get(e), w[e]) : scale.of<false, true>(s[c].get(e), w[e]);
+            }
+            store_block<FORMAT>(v, (int64_t)row * a.d + at, a.codes, a.scales);
+        }
     }
 }
 
@@ -207,17 +255,17 @@ __global__ __launch_bounds__(NT) void k_rms_norm_any(NormArgs a) {
         if (a.sum) sum[i] = (T)s;
         squares = fma((double)s, (double)s, squares);
     }
-    const Scale scale(workgroup_sum(squares, lds) / a.d + a.eps);
+    const Scale scale(workgroup_sum<NT>(squares, lds) / a.d + a.eps);
     for (int i = threadIdx.x; i < a.d; i += NT) {
         // (a sum may have replaced x or delta; this thread wrote it)
         float s = a.sum ? (float)sum[i] : (float)x[i];
         if (!a.sum && a.ddtype != NONE) s = rounded<XT>(s + element(delta, a.ddtype, i));
         const float w = a.wdtype == NONE ? 1.0f : element(a.weight, a.wdtype, i);
-        float odd;
-        const float v = scale.of<false>(s, w, odd);
-        if (a.y) y[i] = (T)(XT == F16 ? odd : v);
+        const float v = scale.of<false, false>(s, w);
+        if (a.y) y[i] = (T)v;
         if (a.format != NONE) {
             // d % 32 == 0: 32 lanes hold a block
+            const float odd = scale.of<false, true>(s, w);
             unsigned top = magnitude_bits(odd);
 #pragma unroll
             for (int m = 1; m < 32; m *= 2) top = max(top, (unsigned)__shfl_xor((int)top, m));
@@ -250,59 +298,78 @@ struct ConvertArgs {
     int rows, cols, log;
 };
 
-template <int XT, int FMT, bool VEC>
+template <int XT, int FMT, bool VEC, int ROWS>
 __global__ __launch_bounds__(NT) void k_mx_quantize(ConvertArgs a) {
     constexpr int ES = XT == F16 ? 2 : 4;
     const int at = ((int)blockIdx.y << a.log | (int)(threadIdx.x & ((1u << a.log) - 1))) * 8;
     if (at >= a.cols) return;
-    const int per = NT >> a.log;
-    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += gridDim.x * per) {
-        float v[8];
-        load8<XT, VEC>(a.x + row * a.stride + (int64_t)at * ES, v);
-        store_block<FMT>(v, (int64_t)row * a.cols + at, a.codes, a.scales);
+    const int per = NT >> a.log, step = gridDim.x * per;
+    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += step * ROWS) {
+        float v[ROWS][8];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (row + i * step < a.rows) load8<XT, VEC>(a.x + (int64_t)(row + i * step) * a.stride + (int64_t)at * ES, v[i]);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (row + i * step < a.rows) store_block<FMT>(v[i], (int64_t)(row + i * step) * a.cols + at, a.codes, a.scales);
     }
 }
 
-template <int XT, int FMT, bool VEC>
+template <int XT, int FMT, bool VEC, int ROWS>
 __global__ __launch_bounds__(NT) void k_mx_dequantize(ConvertArgs a) {
     constexpr int ES = XT == F16 ? 2 : 4;
     const int at = ((int)blockIdx.y << a.log | (int)(threadIdx.x & ((1u << a.log) - 1))) * 8;
     if (at >= a.cols) return;
-    const int per = NT >> a.log;
-    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += gridDim.x * per) {
-        const int64_t in_all = (int64_t)row * a.cols + at;
-        float v[8];
-        if constexpr (FMT == PI_MXFP8) {
-            const u2 c = *reinterpret_cast<const u2*>(a.codes + in_all);
+    const int per = NT >> a.log, step = gridDim.x * per;
+    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += step * ROWS) {
+        u2 c[ROWS];
+        int scale[ROWS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const auto p = i % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i / 2], true)
-                                     : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i / 2], false);
-                v[2 * i] = p[0], v[2 * i + 1] = p[1];
-            }
-        } else {
-            const unsigned c = *reinterpret_cast<const unsigned*>(a.codes + in_all / 2);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c >> (8 * i), 1.0f, 0);
-                v[2 * i] = p[0], v[2 * i + 1] = p[1];
-            }
+        for (int i = 0; i < ROWS; ++i) {
+            if (row + i * step >= a.rows) continue;
+            const int64_t in_all = (int64_t)(row + i * step) * a.cols + at;
+            if constexpr (FMT == PI_MXFP8)
+                c[i] = *reinterpret_cast<const u2*>(a.codes + in_all);
+            else
+                c[i].x = *reinterpret_cast<const unsigned*>(a.codes + in_all / 2);
+            scale[i] = a.scales[in_all / 32];
         }
-        const int scale = a.scales[in_all / 32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = scale == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[i], scale - 127);
-        store8<XT, VEC>(a.out + row * a.stride + (int64_t)at * ES, v);
+        for (int i = 0; i < ROWS; ++i) {
+            if (row + i * step >= a.rows) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (FMT == PI_MXFP8) {
+                    const auto p = e % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][e / 2], true)
+                                         : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][e / 2], false);
+                    v[2 * e] = p[0], v[2 * e + 1] = p[1];
+                } else {
+                    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i].x >> (8 * e), 1.0f, 0);
+                    v[2 * e] = p[0], v[2 * e + 1] = p[1];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = scale[i] == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[e], scale[i] - 127);
+            store8<XT, VEC>(a.out + (int64_t)(row + i * step) * a.stride + (int64_t)at * ES, v);
+        }
     }
 }
 
-template <bool QUANTIZE, int XT, int FMT, bool VEC>
-pi_status launch_convert(const ConvertArgs& a, hipStream_t s) {
-    const int per = NT >> a.log;
+// Several rows of a thread are in flight at once where there are enough for it: 8192 workgroups otherwise.
+template <bool QUANTIZE, int XT, int FMT, bool VEC, int ROWS>
+pi_status launch_rows(const ConvertArgs& a, hipStream_t s) {
+    const int per = (NT >> a.log) * ROWS;
     const dim3 grid(std::min((a.rows + per - 1) / per, 1 << 16), ((a.cols / 8) + (1 << a.log) - 1) >> a.log);
     if constexpr (QUANTIZE)
-        return launch(PI_K_MX_CONVERT, k_mx_quantize<XT, FMT, VEC>, grid, dim3(NT), 0, s, a);
+        return launch(PI_K_MX_CONVERT, k_mx_quantize<XT, FMT, VEC, ROWS>, grid, dim3(NT), 0, s, a);
     else
-        return launch(PI_K_MX_CONVERT, k_mx_dequantize<XT, FMT, VEC>, grid, dim3(NT), 0, s, a);
+        return launch(PI_K_MX_CONVERT, k_mx_dequantize<XT, FMT, VEC, ROWS>, grid, dim3(NT), 0, s, a);
+}
+template <bool QUANTIZE, int XT, int FMT, bool VEC>
+pi_status launch_convert(const ConvertArgs& a, hipStream_t s) {
+    const bool many = (int64_t)a.rows * a.cols >= (int64_t)8192 * NT * 8;
+    return many ? launch_rows<QUANTIZE, XT, FMT, VEC, 4>(a, s) : launch_rows<QUANTIZE, XT, FMT, VEC, 1>(a, s);
 }
 
 template <bool QUANTIZE>
@@ -338,22 +405,24 @@ pi_status check_matrix(const void* data, int64_t stride, int dtype, const pi_mx*
 
 template <int XT, int TPR, int C>
 pi_status launch_norm(const NormArgs& a, hipStream_t s) {
-    constexpr int PER = NT / TPR;
-    return launch(PI_K_NORM, k_rms_norm<XT, TPR, C>, dim3((a.rows + PER - 1) / PER), dim3(NT), 0, s, a);
+    constexpr int PER = std::max(NT / TPR, 1);
+    const dim3 grid((a.rows + PER - 1) / PER), block(std::max(NT, TPR));
+    if (a.format == PI_MXFP8) return launch(PI_K_NORM, k_rms_norm<XT, TPR, C, PI_MXFP8>, grid, block, 0, s, a);
+    if (a.format == PI_MXFP4) return launch(PI_K_NORM, k_rms_norm<XT, TPR, C, PI_MXFP4>, grid, block, 0, s, a);
+    return launch(PI_K_NORM, k_rms_norm<XT, TPR, C, NONE>, grid, block, 0, s, a);
 }
 
 template <int XT>
 pi_status norm_by_size(const NormArgs& a, bool vec, hipStream_t s) {
-    if (!vec || a.d > 8 * NT * 8)
-        return launch(PI_K_NORM, k_rms_norm_any<XT>, dim3(a.rows), dim3(NT), 0, s, a);
+    if (!vec || a.d > 8 * 2048) return launch(PI_K_NORM, k_rms_norm_any<XT>, dim3(a.rows), dim3(NT), 0, s, a);
     if (a.d <= 64) return launch_norm<XT, 8, 1>(a, s);
     if (a.d <= 128) return launch_norm<XT, 16, 1>(a, s);
     if (a.d <= 256) return launch_norm<XT, 32, 1>(a, s);
     if (a.d <= 512) return launch_norm<XT, 64, 1>(a, s);
-    if (a.d <= 8 * NT) return launch_norm<XT, NT, 1>(a, s);
-    if (a.d <= 8 * NT * 2) return launch_norm<XT, NT, 2>(a, s);
-    if (a.d <= 8 * NT * 4) return launch_norm<XT, NT, 4>(a, s);
-    return launch_norm<XT, NT, 8>(a, s);
+    if (a.d <= 2048) return launch_norm<XT, 256, 1>(a, s);
+    if (a.d <= 4096) return launch_norm<XT, 512, 1>(a, s);
+    if (a.d <= 8192) return launch_norm<XT, 1024, 1>(a, s);
+    return launch_norm<XT, 1024, 2>(a, s);
 }
 
 // rows of an operand, and whether all of them are 16-byte aligned

@@ -17,7 +17,8 @@ constexpr int ST = 512;                  // threads of a workgroup
 constexpr int EACH = 8;                  // logits of a thread and step
 constexpr int BINS = 2048;               // of a row's histogram
 constexpr int LIST = 4096;               // tokens in the bins that a rule's border lies in
-constexpr int MOST_CHUNKS = 256;         // of a row: 2^20 logits in chunks of 4096
+constexpr int BLOCK = ST * EACH;         // logits of a workgroup and step: sums are kept for each
+constexpr int MOST_BLOCKS = 256;         // of a row: 2^20 logits
 
 typedef unsigned long long u64;
 constexpr int FRACTION = 43;             // weights are integers of 2^-43: 2^20 of them sum below 2^63
@@ -34,7 +35,7 @@ struct SampleArgs {
     float* prob;
     int* kept;
     int rows, vocab;
-    int chunks, chunk;                   // of a row; logits of one (a multiple of ST * EACH)
+    int chunks, chunk, blocks;           // workgroups of a row, logits of one (a multiple of BLOCK); blocks of a row
     uint8_t* ws;
     int64_t row_bytes;                   // of ws
 };
@@ -45,15 +46,17 @@ struct Top {
     int at, count;                       // lowest index of the largest; tokens that may be kept
 };
 struct RowState {
-    unsigned listed, done;               // tokens in the list, workgroups that have finished
+    u64 mass_lo, p_before;               // weights before k_bin and before the lowest bin of top-p's border
+    int k_bin, k_before;
+    unsigned listed;                     // tokens in the list
 };
 constexpr int64_t WS_STATE = 0;
 constexpr int64_t WS_TOPS = 256;                                   // Top [chunks]
-constexpr int64_t WS_MASS = WS_TOPS + MOST_CHUNKS * 16;            // u64 [BINS]
+constexpr int64_t WS_MASS = WS_TOPS + MOST_BLOCKS * 16;            // u64 [BINS]
 constexpr int64_t WS_COUNT = WS_MASS + BINS * 8;                   // unsigned [BINS]
-constexpr int64_t WS_CHUNK_MASS = WS_COUNT + BINS * 4;             // u64 [chunks]
-constexpr int64_t WS_CHUNK_KEPT = WS_CHUNK_MASS + MOST_CHUNKS * 8; // unsigned [chunks]
-constexpr int64_t WS_LIST = WS_CHUNK_KEPT + MOST_CHUNKS * 4;       // u64 [LIST]: key above the index's complement
+constexpr int64_t WS_BLOCK_MASS = WS_COUNT + BINS * 4;             // u64 [blocks]
+constexpr int64_t WS_BLOCK_KEPT = WS_BLOCK_MASS + MOST_BLOCKS * 8; // unsigned [blocks]
+constexpr int64_t WS_LIST = WS_BLOCK_KEPT + MOST_BLOCKS * 4;       // u64 [LIST]: key above the index's complement
 constexpr int64_t WS_ROW = WS_LIST + LIST * 8;
 
 // A logit as an unsigned integer in the same order; 0 for -inf and NaN, which are never kept.  -0 and 0 are equal.
@@ -228,15 +231,17 @@ __device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* m
 // ---- a row by many workgroups --------------------------------------------------------
 //
 // The logits' bytes would take a microsecond or two; what there is to do is to keep a row's pieces busy at the same time,
-// and to read them few times.  Three launches, a workgroup to each chunk of a row:
+// and to read them few times.  Four launches, a workgroup to each chunk of a row but in the last:
 //   k_sample_top     the largest and smallest logit of the chunk
 //   k_sample_count   with the row's largest known: the chunk's part of a histogram of the distance to it (counts for top-k,
 //                    sums of weights for top-p); without either rule the sum of its weights
-//   k_sample_pick    from the histogram the bins in which the border of top-k and of top-p can lie: sums over the tokens
-//                    above them, and a list of the tokens in them; the row's last workgroup sorts the list, finds the border and
-//                    the token
+//   k_sample_list    from the histogram the bins in which the border of top-k and of top-p can lie: sums over the tokens
+//                    above them, and a list of the tokens in them (left out where no row has either rule)
+//   k_sample_pick    a workgroup to each row: sorts the list, finds the border and the token.  (As a part of the launch before,
+//                    by the row's last workgroup, it took 26 us instead of 5 and 64 rows 108: that needs fences between the
+//                    dies, which write back and drop whole caches.)
 // Sums are integers, so that neither their order nor that of the list matters.  A row whose border bins hold more than
-// LIST tokens (equal logits, or a border far below the others) is done by its last workgroup alone, from the start.
+// LIST tokens (equal logits, or a border far below the others) is done by k_sample_pick alone, from the start.
 
 // 8 logits from i on; those past the row's end are -inf
 template <int DT>
@@ -282,7 +287,7 @@ __global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
         reinterpret_cast<u64*>(ws + WS_MASS)[b] = 0;
         reinterpret_cast<unsigned*>(ws + WS_COUNT)[b] = 0;
     }
-    if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<RowState*>(ws + WS_STATE) = RowState{0u, 0u};
+    if (blockIdx.x == 0 && tid == 0) reinterpret_cast<RowState*>(ws + WS_STATE)->listed = 0;
 
     // the smallest key as the largest of the complements
     unsigned most = 0, low = 0, at = 0;
@@ -355,12 +360,28 @@ struct Binning {
     }
 };
 
+// adds what the workgroup's threads have to a block's sum of weights and count
+__device__ __forceinline__ void add_block(u64 sum, unsigned n, u64* mass, unsigned* count) {
+    if (!__any(n != 0)) return;
+    sum = wave_sum(sum);
+    n = (unsigned)wave_sum((u64)n);
+    if (threadIdx.x % WAVE == 0) atomicAdd(mass, sum), atomicAdd(count, n);
+}
+
+// the sums of this workgroup's blocks to the workspace
+__device__ __forceinline__ void store_blocks(const SampleArgs& a, uint8_t* ws, const u64* mass, const unsigned* count) {
+    const int first = blockIdx.x * (a.chunk / BLOCK);
+    for (int b = threadIdx.x; b < a.chunk / BLOCK && first + b < a.blocks; b += ST) {
+        reinterpret_cast<u64*>(ws + WS_BLOCK_MASS)[first + b] = mass[b];
+        reinterpret_cast<unsigned*>(ws + WS_BLOCK_KEPT)[first + b] = count[b];
+    }
+}
+
 template <int DT>
 __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     __shared__ u64 s_mass[BINS];
     __shared__ unsigned s_count[BINS];
     __shared__ Top s_top;
-    __shared__ u64 s_sum;
     const int row = blockIdx.y, tid = threadIdx.x;
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     uint8_t* ws = a.ws + row * a.row_bytes;
@@ -372,28 +393,23 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
     const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
     if (!by_count && !by_mass) {
-        u64 sum = 0;
-        unsigned n = 0;
-        for (int i = from + tid * EACH; i < to; i += ST * EACH) {
+        for (int b = tid; b < MOST_BLOCKS; b += ST) s_mass[b] = 0, s_count[b] = 0;
+        __syncthreads();
+        for (int base = from, b = 0; base < to; base += BLOCK, ++b) {
+            u64 sum = 0;
+            unsigned n = 0;
             float v[EACH];
-            load_logits<DT>(l, i, a.vocab, v);
+            load_logits<DT>(l, base + tid * EACH, a.vocab, v);
 #pragma unroll
             for (int e = 0; e < EACH; ++e) {
                 if (!order_key(v[e])) continue;
                 const double w = rule.weight(v[e]);
                 if (w >= rule.min_p) sum += fixed(w), ++n;
             }
+            add_block(sum, n, &s_mass[b], &s_count[b]);
         }
-        if (tid == 0) s_sum = 0, s_count[0] = 0;
         __syncthreads();
-        sum = wave_sum(sum);
-        n = (unsigned)wave_sum((u64)n);
-        if (tid % WAVE == 0) atomicAdd(&s_sum, sum), atomicAdd(&s_count[0], n);
-        __syncthreads();
-        if (tid == 0) {
-            reinterpret_cast<u64*>(ws + WS_CHUNK_MASS)[blockIdx.x] = s_sum;
-            reinterpret_cast<unsigned*>(ws + WS_CHUNK_KEPT)[blockIdx.x] = s_count[0];
-        }
+        store_blocks(a, ws, s_mass, s_count);
         return;
     }
     const Binning bin(rule, t);
@@ -433,24 +449,126 @@ __device__ __forceinline__ void find_bin(u64 want, u64 before, const u64* own, i
 }
 
 template <int DT>
-__global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
-    __shared__ u64 s_list[LIST];
+__global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     __shared__ u64 scan[ST / WAVE];
-    __shared__ u64 s_mass[MOST_CHUNKS];
-    __shared__ unsigned s_kept[MOST_CHUNKS];
+    __shared__ u64 s_mass[MOST_BLOCKS];
+    __shared__ unsigned s_kept[MOST_BLOCKS];
     __shared__ Top s_top;
     __shared__ int s_bin[3];
-    __shared__ u64 s_at[5];
-    __shared__ u64 s_sum;
-    __shared__ unsigned s_n, s_last;
+    __shared__ u64 s_at[4];
     const int row = blockIdx.y, tid = threadIdx.x;
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     uint8_t* ws = a.ws + row * a.row_bytes;
     RowState* state = reinterpret_cast<RowState*>(ws + WS_STATE);
     Rule rule = rule_of(a, row);
+    if (rule.greedy || (rule.top_k == 0 && rule.top_p >= 1.0)) return;
+    const Top t = row_top(a, ws, &s_top);
+    rule.top = key_logit(t.most);
+    if (rule.top_k >= t.count) rule.top_k = 0;
+    const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
+    if (t.most == 0 || !(by_count || by_mass)) return;
+    const Binning bin(rule, t);
+
+    // Bins: k_bin holds the border of top-k; the sum that top-p is a part of lies between those without and with it, so the
+    // border of top-p lies in p_lo .. p_hi.
+    int k_bin = BINS, p_lo = BINS, p_hi = BINS;
+    u64 k_before = 0, mass_lo = 0, p_before = 0;      // tokens before k_bin, weights before it and before p_lo
+    u64 n[BINS / ST], m[BINS / ST], own_n = 0, own_m = 0, all_n, all_m;
+#pragma unroll
+    for (int e = 0; e < BINS / ST; ++e) {
+        n[e] = reinterpret_cast<const unsigned*>(ws + WS_COUNT)[tid * (BINS / ST) + e];
+        m[e] = reinterpret_cast<const u64*>(ws + WS_MASS)[tid * (BINS / ST) + e];
+        own_n += n[e], own_m += m[e];
+    }
+    const u64 before_n = before_and_total<u64>(own_n, scan, all_n), before_m = before_and_total<u64>(own_m, scan, all_m);
+    if (tid < 3) s_bin[tid] = BINS;
+    __syncthreads();
+    if (by_count) find_bin((u64)rule.top_k, before_n, n, &s_bin[0]);
+    __syncthreads();
+    k_bin = s_bin[0];
+    if (tid == 0) s_at[0] = s_at[2] = 0, s_at[1] = s_at[3] = all_m;
+    __syncthreads();
+    if (k_bin < BINS && k_bin / (BINS / ST) == tid) {
+        u64 c = before_n, w = before_m;
+        for (int e = 0; e < k_bin % (BINS / ST); ++e) c += n[e], w += m[e];
+        s_at[0] = c, s_at[1] = w, s_at[3] = w + m[k_bin % (BINS / ST)];
+    }
+    __syncthreads();
+    k_before = s_at[0], mass_lo = s_at[1];
+    if (by_mass) {
+        const double lo = ceil(rule.top_p * (double)mass_lo), hi = ceil(rule.top_p * (double)s_at[3]);
+        find_bin(lo > 1.0 ? (u64)lo : 1, before_m, m, &s_bin[1]);
+        find_bin(hi > 1.0 ? (u64)hi : 1, before_m, m, &s_bin[2]);
+        __syncthreads();
+        p_lo = s_bin[1], p_hi = s_bin[2];
+        if (p_lo < BINS && p_lo / (BINS / ST) == tid) {
+            u64 w = before_m;
+            for (int e = 0; e < p_lo % (BINS / ST); ++e) w += m[e];
+            s_at[2] = w;
+        }
+        __syncthreads();
+        p_before = s_at[2];
+    }
+    if (blockIdx.x == 0 && tid == 0) state->mass_lo = mass_lo, state->p_before = p_before, state->k_bin = k_bin, state->k_before = (int)k_before;
+    const int border = by_mass ? p_lo : k_bin;           // bins before it are kept for certain
+
+    for (int b = tid; b < MOST_BLOCKS; b += ST) s_mass[b] = 0, s_kept[b] = 0;
+    __syncthreads();
+    const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
+    for (int base = from, block = 0; base < to; base += BLOCK, ++block) {
+        u64 sum = 0;
+        unsigned n = 0, in_list = 0;               // (a bit for each)
+        float v[EACH];
+        load_logits<DT>(l, base + tid * EACH, a.vocab, v);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            if (!order_key(v[e])) continue;
+            const int b = bin.of(v[e]);
+            if (b < border) {
+                const double w = rule.weight(v[e]);
+                if (w >= rule.min_p) sum += fixed(w), ++n;
+            } else if (b == k_bin || (by_mass && b <= p_hi)) {
+                in_list |= 1u << e;
+            }
+        }
+        // one place in the list's count for a wave's tokens: each addition to it waits for the one before
+        if (__any(in_list != 0)) {
+            const int mine = __popc(in_list), incl = wave_incl_scan(mine);
+            unsigned at = 0;
+            if (tid % WAVE == WAVE - 1) at = atomicAdd(&state->listed, (unsigned)incl);
+            at = __shfl(at, WAVE - 1) + incl - mine;
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) {
+                if (!(in_list >> e & 1)) continue;
+                if (at < LIST)
+                    reinterpret_cast<u64*>(ws + WS_LIST)[at] = (u64)order_key(v[e]) << 32 | ~(unsigned)(base + tid * EACH + e);
+                ++at;
+            }
+        }
+        add_block(sum, n, &s_mass[block], &s_kept[block]);
+    }
+    __syncthreads();
+    store_blocks(a, ws, s_mass, s_kept);
+}
+
+// The token of a row: a workgroup each.
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
+    __shared__ u64 s_list[LIST];
+    __shared__ u64 scan[ST / WAVE];
+    __shared__ u64 s_mass[MOST_BLOCKS];
+    __shared__ unsigned s_kept[MOST_BLOCKS];
+    __shared__ Top s_top;
+    __shared__ u64 s_sum;
+    __shared__ unsigned s_n;
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
+    const uint8_t* ws = a.ws + row * a.row_bytes;
+    const RowState state = *reinterpret_cast<const RowState*>(ws + WS_STATE);
+    Rule rule = rule_of(a, row);
     const Top t = row_top(a, ws, &s_top);
     if (t.most == 0 || rule.greedy) {
-        if (blockIdx.x == 0 && tid == 0) {
+        if (tid == 0) {
             a.token[row] = t.most ? t.at : -1;
             if (a.prob) a.prob[row] = t.most ? 1.0f : 0.0f;
             if (a.kept) a.kept[row] = t.most ? 1 : 0;
@@ -461,117 +579,42 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     if (rule.top_k >= t.count) rule.top_k = 0;
     const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
     const Binning bin(rule, t);
-
-    // Bins: k_bin holds the border of top-k; the sum that top-p is a part of lies between those without and with it, so the
-    // border of top-p lies in p_lo .. p_hi.
-    int k_bin = BINS, p_lo = BINS, p_hi = BINS;
-    u64 k_before = 0, mass_lo = 0, p_before = 0;      // tokens before k_bin, weights before it and before p_lo
-    if (by_count || by_mass) {
-        u64 n[BINS / ST], m[BINS / ST], own_n = 0, own_m = 0, all_n, all_m;
-#pragma unroll
-        for (int e = 0; e < BINS / ST; ++e) {
-            n[e] = reinterpret_cast<const unsigned*>(ws + WS_COUNT)[tid * (BINS / ST) + e];
-            m[e] = reinterpret_cast<const u64*>(ws + WS_MASS)[tid * (BINS / ST) + e];
-            own_n += n[e], own_m += m[e];
-        }
-        const u64 before_n = before_and_total<u64>(own_n, scan, all_n), before_m = before_and_total<u64>(own_m, scan, all_m);
-        if (tid < 3) s_bin[tid] = BINS;
-        __syncthreads();
-        if (by_count) find_bin((u64)rule.top_k, before_n, n, &s_bin[0]);
-        __syncthreads();
-        k_bin = s_bin[0];
-        if (tid == 0) s_at[0] = s_at[2] = 0, s_at[1] = s_at[3] = all_m;
-        __syncthreads();
-        if (k_bin < BINS && k_bin / (BINS / ST) == tid) {
-            u64 c = before_n, w = before_m;
-            for (int e = 0; e < k_bin % (BINS / ST); ++e) c += n[e], w += m[e];
-            s_at[0] = c, s_at[1] = w, s_at[3] = w + m[k_bin % (BINS / ST)];
-        }
-        __syncthreads();
-        k_before = s_at[0], mass_lo = s_at[1];
-        if (by_mass) {
-            const double lo = ceil(rule.top_p * (double)mass_lo), hi = ceil(rule.top_p * (double)s_at[3]);
-            find_bin(lo > 1.0 ? (u64)lo : 1, before_m, m, &s_bin[1]);
-            find_bin(hi > 1.0 ? (u64)hi : 1, before_m, m, &s_bin[2]);
-            __syncthreads();
-            p_lo = s_bin[1], p_hi = s_bin[2];
-            if (p_lo < BINS && p_lo / (BINS / ST) == tid) {
-                u64 w = before_m;
-                for (int e = 0; e < p_lo % (BINS / ST); ++e) w += m[e];
-                s_at[2] = w;
-            }
-            __syncthreads();
-            p_before = s_at[2];
-        }
-    }
-    const int border = by_mass ? p_lo : k_bin;           // bins before it are kept for certain
-
-    if (by_count || by_mass) {
-        if (tid == 0) s_sum = 0, s_n = 0;
-        __syncthreads();
-        u64 sum = 0;
-        unsigned n = 0;
-        const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
-        for (int i = from + tid * EACH; i < to; i += ST * EACH) {
-            float v[EACH];
-            load_logits<DT>(l, i, a.vocab, v);
-#pragma unroll
-            for (int e = 0; e < EACH; ++e) {
-                const unsigned key = order_key(v[e]);
-                if (!key) continue;
-                const int b = bin.of(v[e]);
-                if (b < border) {
-                    const double w = rule.weight(v[e]);
-                    if (w >= rule.min_p) sum += fixed(w), ++n;
-                } else if (b == k_bin || (by_mass && b <= p_hi)) {
-                    const unsigned at = atomicAdd(&state->listed, 1u);
-                    if (at < LIST) reinterpret_cast<u64*>(ws + WS_LIST)[at] = (u64)key << 32 | ~(unsigned)(i + e);
-                }
-            }
-        }
-        sum = wave_sum(sum);
-        n = (unsigned)wave_sum((u64)n);
-        if (tid % WAVE == 0 && n) atomicAdd(&s_sum, sum), atomicAdd(&s_n, n);
-        __syncthreads();
-        if (tid == 0) {
-            reinterpret_cast<u64*>(ws + WS_CHUNK_MASS)[blockIdx.x] = s_sum;
-            reinterpret_cast<unsigned*>(ws + WS_CHUNK_KEPT)[blockIdx.x] = s_n;
-        }
-    }
-
-    // the row's last workgroup goes on
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&state->done, 1u) == (unsigned)a.chunks - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const unsigned listed = __hip_atomic_load(&state->listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int k_bin = state.k_bin;
+    const u64 k_before = (u64)state.k_before, mass_lo = state.mass_lo, p_before = state.p_before;
+    const unsigned listed = by_count || by_mass ? state.listed : 0;
     if (listed > LIST) {
         whole_row<DT>(a, row, rule, s_list, scan);
         return;
     }
-    for (int c = tid; c < a.chunks; c += ST) {
-        s_mass[c] = __hip_atomic_load(reinterpret_cast<u64*>(ws + WS_CHUNK_MASS) + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_kept[c] = __hip_atomic_load(reinterpret_cast<unsigned*>(ws + WS_CHUNK_KEPT) + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int b = tid; b < a.blocks; b += ST) {
+        s_mass[b] = reinterpret_cast<const u64*>(ws + WS_BLOCK_MASS)[b];
+        s_kept[b] = reinterpret_cast<const unsigned*>(ws + WS_BLOCK_KEPT)[b];
     }
-    // the list, largest first
+    // the list, largest first: short ones by counting the larger ones of each, long ones by a bitonic network
     int size = WAVE;
     while (size < (int)listed) size *= 2;
     for (int i = tid; i < size; i += ST)
-        s_list[i] = i < (int)listed
-                        ? __hip_atomic_load(reinterpret_cast<u64*>(ws + WS_LIST) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                        : 0ull;
+        s_list[i] = i < (int)listed ? reinterpret_cast<const u64*>(ws + WS_LIST)[i] : 0ull;
     __syncthreads();
-    for (int run = 2; listed > 1 && run <= size; run *= 2)
-        for (int step = run / 2; step > 0; step /= 2) {
-            for (int i = tid; i < size / 2; i += ST) {
-                const int x = 2 * i - (i & (step - 1)), y = x + step;
-                const u64 p = s_list[x], q = s_list[y];
-                if ((p < q) == ((x & run) == 0)) s_list[x] = q, s_list[y] = p;
+    if (listed <= ST) {
+        const u64 mine = tid < (int)listed ? s_list[tid] : 0;
+        int rank = 0;
+#pragma unroll 8
+        for (int i = 0; i < (int)listed; ++i) rank += s_list[i] > mine;
+        __syncthreads();
+        if (tid < (int)listed) s_list[rank] = mine;
+        __syncthreads();
+    } else {
+        for (int run = 2; run <= size; run *= 2)
+            for (int step = run / 2; step > 0; step /= 2) {
+                for (int i = tid; i < size / 2; i += ST) {
+                    const int x = 2 * i - (i & (step - 1)), y = x + step;
+                    const u64 p = s_list[x], q = s_list[y];
+                    if ((p < q) == ((x & run) == 0)) s_list[x] = q, s_list[y] = p;
+                }
+                __syncthreads();
             }
-            __syncthreads();
-        }
+    }
 
     // How many of the list are kept: a prefix.  Its tokens of k_bin are the last; top-k keeps top_k - k_before of them.
     unsigned last_key = 1, last_at = 0xffffffffu;        // the last token kept
@@ -625,56 +668,60 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
         last_key = (unsigned)(last >> 32), last_at = ~(unsigned)last;
         for (int i = tid; i < keep; i += ST) {
             const double x = rule.weight(key_logit((unsigned)(s_list[i] >> 32)));
-            const int c = (int)(~(unsigned)s_list[i]) / a.chunk;
-            if (x >= rule.min_p) atomicAdd(&s_mass[c], fixed(x)), atomicAdd(&s_kept[c], 1u);
+            const int b = (int)(~(unsigned)s_list[i]) / BLOCK;
+            if (x >= rule.min_p) atomicAdd(&s_mass[b], fixed(x)), atomicAdd(&s_kept[b], 1u);
         }
         __syncthreads();
     } else {
         __syncthreads();
     }
 
-    // the chunk that the random number falls into
+    // the block that the random number falls into
     u64 total, kept;
-    const u64 mine = tid < a.chunks ? s_mass[tid] : 0;
+    const u64 mine = tid < a.blocks ? s_mass[tid] : 0;
     const u64 before = before_and_total<u64>(mine, scan, total);
-    before_and_total<u64>(tid < a.chunks ? (u64)s_kept[tid] : 0ull, scan, kept);
+    before_and_total<u64>(tid < a.blocks ? (u64)s_kept[tid] : 0ull, scan, kept);
     const float u = a.u[row];
     u64 target = u > 0.0f ? (u64)((double)u * (double)total) : 0;
     if (u >= 1.0f || target >= total) target = total - 1;
     if (tid == 0 && a.kept) a.kept[row] = (int)kept;
     if (before <= target && target < before + mine) s_n = tid, s_sum = before;
     __syncthreads();
-    // and the token in it: every thread a run
-    const int run = a.chunk / ST, from = (int)s_n * a.chunk + tid * run, to = min(from + run, a.vocab);
-    auto weight = [&](int i) __attribute__((always_inline)) {
-        const float x = logit<DT>(l, i);
-        const unsigned key = order_key(x);
-        if (key < last_key || (key == last_key && (unsigned)i > last_at)) return 0ull;
-        const double w = rule.weight(x);
-        return w >= rule.min_p ? (u64)fixed(w) : 0ull;
-    };
-    u64 sum = 0, in_chunk;
-    for (int i = from; i < to; ++i) sum += weight(i);
-    u64 at = s_sum + before_and_total<u64>(sum, scan, in_chunk);
-    if (target < at || target >= at + sum) return;
-    for (int i = from; i < to; ++i) {
-        const u64 w = weight(i);
-        at += w;
-        if (at > target) {
-            a.token[row] = i;
-            if (a.prob) a.prob[row] = (float)((double)w / (double)total);
-            return;
+    // and the token in it: every thread has a run of eight
+    const int from = (int)s_n * BLOCK + tid * EACH;
+    float v[EACH];
+    load_logits<DT>(l, from, a.vocab, v);
+    u64 w[EACH], sum = 0, in_block;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const unsigned key = order_key(v[e]);
+        w[e] = 0;
+        if (key > last_key || (key == last_key && (unsigned)(from + e) <= last_at)) {
+            const double x = rule.weight(v[e]);
+            w[e] = x >= rule.min_p ? fixed(x) : 0;
         }
+        sum += w[e];
+    }
+    u64 at = s_sum + before_and_total<u64>(sum, scan, in_block);
+    if (target < at || target >= at + sum) return;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        if (target >= at && target < at + w[e]) {
+            a.token[row] = from + e;
+            if (a.prob) a.prob[row] = (float)((double)w[e] / (double)total);
+        }
+        at += w[e];
     }
 }
 
 size_t sample_bytes(int rows, int) { return (size_t)rows * WS_ROW; }
 
-// Chunks of a row so that some 512 workgroups have work, of 4096 logits at least (eight for a thread).
+// Chunks of a row so that some 512 workgroups have work, of 4096 logits at least.
 void chunks_of(SampleArgs& a) {
-    const int step = ST * EACH, want = std::max(1, 512 / a.rows);
-    a.chunk = std::max(1, (int)(((int64_t)a.vocab + (int64_t)want * step - 1) / ((int64_t)want * step))) * step;
+    const int want = std::max(1, 512 / a.rows);
+    a.chunk = std::max(1, (int)(((int64_t)a.vocab + (int64_t)want * BLOCK - 1) / ((int64_t)want * BLOCK))) * BLOCK;
     a.chunks = (a.vocab + a.chunk - 1) / a.chunk;
+    a.blocks = (a.vocab + BLOCK - 1) / BLOCK;
 }
 
 template <int DT>
@@ -682,7 +729,8 @@ pi_status sample(const SampleArgs& a, hipStream_t s) {
     const dim3 grid(a.chunks, a.rows), block(ST);
     TRY(launch(PI_K_SAMPLE, k_sample_top<DT>, grid, block, 0, s, a));
     TRY(launch(PI_K_SAMPLE, k_sample_count<DT>, grid, block, 0, s, a));
-    return launch(PI_K_SAMPLE, k_sample_pick<DT>, grid, block, 0, s, a);
+    if (a.top_k || a.top_p) TRY(launch(PI_K_SAMPLE, k_sample_list<DT>, grid, block, 0, s, a));
+    return launch(PI_K_SAMPLE, k_sample_pick<DT>, dim3(a.rows), block, 0, s, a);
 }
 
 }  // namespace
@@ -712,7 +760,7 @@ pi_status pi_sample(const void* logits, int32_t rows, int32_t vocab, int64_t row
           sample_bytes(rows, vocab));
     CHECK(aligned(ws, 256), PI_ERR_ALIGN, "sample: workspace must be 256-byte aligned");
     SampleArgs a{(const uint8_t*)logits, row_stride, rule->temperature, rule->top_k, rule->top_p, rule->min_p, u, token, prob,
-                 kept, rows, vocab, 0, 0, (uint8_t*)ws, WS_ROW};
+                 kept, rows, vocab, 0, 0, 0, (uint8_t*)ws, WS_ROW};
     chunks_of(a);
     return dtype == PI_F16 ? sample<F16>(a, (hipStream_t)stream) : sample<F32>(a, (hipStream_t)stream);
 }
