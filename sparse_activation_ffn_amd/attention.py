@@ -3,18 +3,19 @@ through the C ABI: the cache with its pages' bookkeeping, one layer's attention
 (rotary append, then attention of the new tokens), and a whole decoder layer with
 the predictor-gated sparse FFN as its other half.
 
-Only torch allocations, plain matrix products (the projections) and C calls happen
-here.  Bookkeeping stays on the device: nothing waits for a result.
+Only torch allocations, plain matrix products (projections with plain weights) and C
+calls happen here.  Bookkeeping stays on the device: nothing waits for a result.
 """
 from __future__ import annotations
 
 import math
-from typing import Optional, Sequence
+from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import binding as pb
 from .layer import DeviceLayer, StepBuffers, decode_step
+from .mx import MxBuffer, MxLinear
 
 
 class PagedCache:
@@ -87,9 +88,10 @@ class PagedCache:
 
 class AttentionLayer:
     """One layer's attention: w_qkv [(q_heads + 2 kv_heads) * head_dim][d], w_o [d][q_heads *
-    head_dim], both in the cache's dtype; rope from pb.make_rope, rule from pb.make_score_rule."""
+    head_dim], tensors in the cache's dtype or MxLinear; rope from pb.make_rope, rule from
+    pb.make_score_rule."""
 
-    def __init__(self, w_qkv: torch.Tensor, w_o: torch.Tensor, q_heads: int, kv_heads: int,
+    def __init__(self, w_qkv: Union[torch.Tensor, MxLinear], w_o: Union[torch.Tensor, MxLinear], q_heads: int, kv_heads: int,
                  rope: pb.Rope, rule: Optional[pb.ScoreRule] = None):
         self.q_heads, self.kv_heads = q_heads, kv_heads
         self.head_dim = w_qkv.shape[0] // (q_heads + 2 * kv_heads)
@@ -97,38 +99,50 @@ class AttentionLayer:
         self.rule = rule or pb.make_score_rule(1.0 / math.sqrt(self.head_dim))
         self.ws: Optional[torch.Tensor] = None
 
-    def heads(self, x: torch.Tensor):
-        """Queries, keys and values of x [tokens][d]: views of one product."""
+    def heads(self, x: Union[torch.Tensor, pb.Mx], dtype=None):
+        """Queries, keys and values of x [tokens][d] (microscaled: for an MxLinear w_qkv, and the
+        result's dtype with it): views of one product."""
         d, hq, hk = self.head_dim, self.q_heads, self.kv_heads
-        y = (x @ self.w_qkv.t()).view(-1, hq + 2 * hk, d)
+        y = self.w_qkv(x, dtype) if isinstance(self.w_qkv, MxLinear) else x @ self.w_qkv.t()
+        y = y.view(-1, hq + 2 * hk, d)
         return y[:, :hq], y[:, hq:hq + hk], y[:, hq + hk:]
 
-    def __call__(self, x: torch.Tensor, cache: PagedCache, layer: int, batch: pb.SeqBatch):
-        q, k, v = self.heads(x)
+    def __call__(self, x: Union[torch.Tensor, pb.Mx], cache: PagedCache, layer: int, batch: pb.SeqBatch):
+        q, k, v = self.heads(x, cache.k.dtype)
         pb.pi_rope_append(cache.cache, layer, batch, self.rope, q, q, k, v)
         need = pb.pi_attention_workspace_bytes(cache.cache, batch, self.q_heads)
         if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            self.ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         pb.pi_paged_attention(cache.cache, layer, batch, self.rule, q, q, None, self.ws)
-        return q.reshape(x.shape[0], self.q_heads * self.head_dim) @ self.w_o.t()
+        if isinstance(self.w_o, MxLinear):
+            return self.w_o(q.flatten(1))                # (a view: the heads of a row lie side by side)
+        return q.reshape(q.shape[0], self.q_heads * self.head_dim) @ self.w_o.t()
 
 
 class DecoderLayer:
     """Attention and the predictor-gated sparse FFN, each after a norm and added to its input:
-    x += attention(norm(x)); x += ffn(norm(x)).  x [tokens][d] in the cache's dtype."""
+    x += attention(norm(x)); x += ffn(norm(x)).  x [tokens][d] in the cache's dtype.
+    norms: the weights [d] of two root-mean-square norms, which take up the additions (step());
+    without them the norms are layer norms without weights."""
 
-    def __init__(self, attention: AttentionLayer, ffn: DeviceLayer, eps: float = 1e-5):
+    def __init__(self, attention: AttentionLayer, ffn: DeviceLayer, eps: float = 1e-5,
+                 norms: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
         self.attention, self.ffn, self.eps = attention, ffn, eps
         self.buffers = {}
+        self.norms = None if norms is None else tuple(pb.make_norm(w, eps) for w in norms)
+        # the first norm's output goes into 8 bits where the projection after it reads them
+        mx = self.norms is not None and isinstance(attention.w_qkv, MxLinear)
+        self.input = MxBuffer(attention.w_qkv.shape[1]) if mx else None
 
     def norm(self, x: torch.Tensor) -> torch.Tensor:
         return torch.nn.functional.layer_norm(x.float(), x.shape[-1:], eps=self.eps).to(x.dtype)
 
-    def feed_forward(self, x: torch.Tensor) -> torch.Tensor:
+    def feed_forward(self, x: torch.Tensor, dtype=None) -> torch.Tensor:
         """The sparse FFN, in runs of at most PI_MAX_BATCH tokens (a call's union of active
-        neurons grows with its tokens)."""
+        neurons grows with its tokens), in x's dtype or `dtype`."""
+        dtype = dtype or x.dtype
         if x.shape[0] == 0:
-            return torch.empty_like(x)
+            return torch.empty_like(x, dtype=dtype)
         # as the FFN is now: a new index, a placement or a threshold replaces what the descriptors name
         predictor, parts = self.ffn.descriptors()
         out = []
@@ -137,9 +151,26 @@ class DecoderLayer:
             if n not in self.buffers or self.buffers[n].lists.n_hot != self.ffn.n_hot:
                 self.buffers[n] = StepBuffers(self.ffn, n, x.device)
             y = decode_step(self.ffn, part.contiguous(), self.buffers[n], predictor, parts)
-            out.append(y.to(x.dtype, copy=True))      # (the buffers are the next run's)
+            out.append(y.to(dtype, copy=True))        # (the buffers are the next run's)
         return torch.cat(out)
 
+    def step(self, x: torch.Tensor, delta: Optional[torch.Tensor], cache: PagedCache, layer: int, batch: pb.SeqBatch):
+        """The layer (of one with `norms`) on the stream x + delta (delta None: x alone): the stream
+        with the attention added, and the FFN's float32 output, which the next layer's first norm
+        or TokenHead adds to it."""
+        h = None if self.input is not None else torch.empty_like(x)
+        mx = None if self.input is None else self.input.rows(x.shape[0], x.device)
+        added = None if delta is None else torch.empty_like(x)
+        pb.pi_rms_norm(self.norms[0], x, delta=delta, sum_out=added, y=h, mx=mx)
+        x = x if added is None else added
+        a = self.attention(mx if h is None else h, cache, layer, batch)
+        added, h = torch.empty_like(x), torch.empty_like(x)
+        pb.pi_rms_norm(self.norms[1], x, delta=a, sum_out=added, y=h)
+        return added, self.feed_forward(h, torch.float32)
+
     def __call__(self, x: torch.Tensor, cache: PagedCache, layer: int, batch: pb.SeqBatch):
+        if self.norms is not None:
+            x, y = self.step(x, None, cache, layer, batch)
+            return (x + y).to(x.dtype)
         x = x + self.attention(self.norm(x), cache, layer, batch)
         return x + self.feed_forward(self.norm(x))
