@@ -209,10 +209,16 @@ def ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def stream_handle(stream=None) -> Optional[int]:
-    if stream is None:
+def stream_handle(stream=None, device: int = -1) -> Optional[int]:
+    """device: the one that a call's tensors lie on, if that is known: it has to be the current one, on whose streams
+    a call runs."""
+    if stream is None or device >= 0:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        here = torch.cuda.current_device()
+        if device >= 0 and device != here:
+            raise ValueError(f"tensors on cuda:{device}, the current device is cuda:{here}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -475,28 +481,30 @@ def pi_pages_copy(cache: KvCache, src, dst, stream=None):
 def pi_rms_norm(norm: Norm, x, delta=None, sum_out=None, y=None, mx: Optional[Mx] = None, stream=None):
     """x, delta, sum_out, y: [tokens][d] or [tokens][heads][d], the elements of a row contiguous, other strides free;
     sum_out and y of x's dtype, delta float32 or float16."""
-    shape, dt = x.shape, dtype_code(x)
-    parts = [_norm_rows(name, t, shape, norm.d, None if name == "delta" else dt)
-             for name, t in (("x", x), ("delta", delta), ("sum_out", sum_out), ("y", y))]
-    heads = 1 if len(shape) == 2 else shape[1]
-    _on_device(getattr(norm, "_keep", None), x, delta, sum_out, y, *getattr(mx, "_keep", ()))
-    _check(lib().pi_rms_norm(C.byref(norm), shape[0], heads, dt, parts[0], 0 if delta is None else dtype_code(delta),
-                             parts[1], parts[2], parts[3], None if mx is None else C.byref(mx),
-                             stream_handle(stream)))
+    shape = x.shape
+    if len(shape) not in (2, 3) or shape[-1] != norm.d:
+        raise ValueError(f"x must be [tokens]([heads])[{norm.d}], got {tuple(shape)}")
+    heads, dt = 1 if len(shape) == 2 else shape[1], x.dtype
+    rows = (_norm_rows("x", x, shape, dt), _norm_rows("delta", delta, shape, None),
+            _norm_rows("sum_out", sum_out, shape, dt), _norm_rows("y", y, shape, dt))
+    device = _on_device((getattr(norm, "_keep", None), x, delta, sum_out, y), mx)
+    _check(lib().pi_rms_norm(C.byref(norm), shape[0], heads, dtype_code(x), rows[0],
+                             0 if delta is None else dtype_code(delta), rows[1], rows[2], rows[3],
+                             None if mx is None else C.byref(mx), stream_handle(stream, device)))
 
 
 def pi_mx_quantize(x, mx: Mx, stream=None):
     """x [mx.rows][mx.cols], the elements of a row contiguous."""
-    _matrix("x", x, mx.rows, mx.cols)
-    _on_device(x, *getattr(mx, "_keep", ()))
-    _check(lib().pi_mx_quantize(ptr(x), x.stride(0), dtype_code(x), C.byref(mx), stream_handle(stream)))
+    stride = _matrix("x", x, mx.rows, mx.cols)
+    device = _on_device((x,), mx)
+    _check(lib().pi_mx_quantize(x.data_ptr(), stride, dtype_code(x), C.byref(mx), stream_handle(stream, device)))
 
 
 def pi_mx_dequantize(mx: Mx, out, stream=None):
     """out [mx.rows][mx.cols], the elements of a row contiguous."""
-    _matrix("out", out, mx.rows, mx.cols)
-    _on_device(out, *getattr(mx, "_keep", ()))
-    _check(lib().pi_mx_dequantize(C.byref(mx), ptr(out), out.stride(0), dtype_code(out), stream_handle(stream)))
+    stride = _matrix("out", out, mx.rows, mx.cols)
+    device = _on_device((out,), mx)
+    _check(lib().pi_mx_dequantize(C.byref(mx), out.data_ptr(), stride, dtype_code(out), stream_handle(stream, device)))
 
 
 def pi_mx_product_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -506,11 +514,11 @@ def pi_mx_product_workspace_bytes(m: int, n: int, k: int) -> int:
 def pi_mx_product(a: Mx, w: Mx, out, bias=None, ws=None, stream=None):
     """out [a.rows][w.rows], the elements of a row contiguous; bias float32 [w.rows] or None; ws of
     pi_mx_product_workspace_bytes(a.rows, w.rows, a.cols) bytes."""
-    _matrix("out", out, a.rows, w.rows)
+    stride = _matrix("out", out, a.rows, w.rows)
     _vector("bias", bias, "float32", w.rows)
-    _on_device(out, bias, ws, *getattr(a, "_keep", ()), *getattr(w, "_keep", ()))
-    _check(lib().pi_mx_product(C.byref(a), C.byref(w), ptr(bias), ptr(out), out.stride(0), dtype_code(out), ptr(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
+    device = _on_device((out, bias, ws), a, w)
+    _check(lib().pi_mx_product(C.byref(a), C.byref(w), ptr(bias), out.data_ptr(), stride, dtype_code(out), ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream, device)))
 
 
 def pi_sample_workspace_bytes(rows: int, vocab: int) -> int:
@@ -521,17 +529,17 @@ def pi_sample(logits, rule: SampleRule, u, token, prob=None, kept=None, ws=None,
     """logits [rows][vocab], the elements of a row contiguous; u float32 [rows]; token int32 [rows], prob float32
     [rows], kept int32 [rows] (the last two may be None)."""
     rows, vocab = logits.shape
-    _matrix("logits", logits, rows, vocab)
+    stride = _matrix("logits", logits, rows, vocab)
     for name, t, dtype in (("u", u, "float32"), ("token", token, "int32"), ("prob", prob, "float32"),
                            ("kept", kept, "int32")):
         _vector(name, t, dtype, rows)
     for t in getattr(rule, "_keep", ()):
         if t is not None and not isinstance(t, int) and t.numel() < rows:
             raise ValueError(f"a rule's list has {t.numel()} entries for {rows} rows")
-    _on_device(logits, u, token, prob, kept, ws, *getattr(rule, "_keep", ()))
-    _check(lib().pi_sample(ptr(logits), rows, vocab, logits.stride(0), dtype_code(logits), C.byref(rule), ptr(u),
+    device = _on_device((logits, u, token, prob, kept, ws), rule)
+    _check(lib().pi_sample(logits.data_ptr(), rows, vocab, stride, dtype_code(logits), C.byref(rule), ptr(u),
                            ptr(token), ptr(prob), ptr(kept), ptr(ws),
-                           0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream)))
+                           0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream, device)))
 
 
 def pi_kernel_timer_start(kid: int, max_launches: int):
@@ -677,32 +685,39 @@ def make_sample_rule(temperature=None, top_k=None, top_p=None, min_p=None) -> Sa
     return r
 
 
-def _matrix(name: str, t, rows: int, cols: int):
-    if len(t.shape) != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{rows}][{cols}] with contiguous rows, got {tuple(t.shape)} with strides "
-                         f"{t.stride()}")
+def _matrix(name: str, t, rows: int, cols: int) -> int:
+    """Refuses a tensor that is not [rows][cols] with contiguous rows; their distance."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or (cols > 1 and strides[1] != 1):
+        raise ValueError(f"{name} must be [{rows}][{cols}] with contiguous rows, got {tuple(shape)} with strides {strides}")
+    return strides[0]
 
 
-def _norm_rows(name: str, t, shape, d: int, dtype):
-    """Reference to [tokens][d] or [tokens][heads][d] as the library sees it, or None."""
+def _norm_rows(name: str, t, shape, dtype):
+    """Reference to rows like x's as the library sees them, or None; dtype None: any that it has."""
     if t is None:
         return None
     strides = t.stride()
-    if len(shape) not in (2, 3) or t.shape != shape or shape[-1] != d or (d > 1 and strides[-1] != 1):
-        raise ValueError(f"{name} must be [tokens]([heads])[{d}] like x {tuple(shape)} with contiguous rows, got "
-                         f"{tuple(t.shape)} with strides {strides}")
-    if dtype is not None and dtype_code(t) != dtype:
+    if t.shape != shape or (strides[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be like x {tuple(shape)} with contiguous rows, got {tuple(t.shape)} with "
+                         f"strides {strides}")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has x's dtype")
     return C.byref(Rows(t.data_ptr(), strides[0], strides[1] if len(shape) == 3 else 0))
 
 
-def _on_device(*tensors):
-    """Refuses tensors (None and addresses pass) that are not on the current device: a kernel on its stream would fault."""
-    import torch
-    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != here:
-            raise ValueError(f"tensor on {t.device}, the current device is cuda:{here}")
+def _on_device(tensors, *descriptors) -> int:
+    """The one CUDA device that tensors (None and addresses pass) and what descriptors keep lie on."""
+    device = -1
+    for group in (tensors, *[getattr(d, "_keep", ()) for d in descriptors]):
+        for t in group:
+            if t is None or isinstance(t, int):
+                continue
+            at = t.get_device()
+            if at < 0 or (device >= 0 and at != device):
+                raise ValueError(f"tensors must be on one CUDA device, got one on {t.device}")
+            device = at
+    return device
 
 
 def _int32(name: str, t, shape):
