@@ -68,6 +68,43 @@ __device__ __forceinline__ float key_logit(unsigned key) {
     return __builtin_bit_cast(float, key >> 31 ? key & 0x7fffffffu : ~key);
 }
 
+// exp for z <= 0 by a table of 2^(j/32) (Tang, ACM TOMS 15(2), 1989): z = (32 m + j) ln 2 / 32 + r with |r| <= ln 2 / 64, exp(z)
+// = 2^m 2^(j/32) exp(r), exp(r) by its series to r^5 (the next term is 2^-49).  Weights are needed to 2^-44; the library's
+// function takes three times the operations, and a row's distribution hundreds of thousands of them.
+__constant__ double EXP2_32[32] = {
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
+
+constexpr double LN2 = 0.693147180559945309417;
+
+struct Exp {
+    const double* table;                 // in LDS
+    // the whole workgroup calls it, a barrier follows before the first use
+    static __device__ void fill(double* lds) {
+        if (threadIdx.x < 32) lds[threadIdx.x] = EXP2_32[threadIdx.x];
+    }
+    __device__ __forceinline__ double operator()(double z) const {
+        if (z < -110.0) return 0.0;      // (below the least float32, which min-p may be)
+        // the nearest integer by the addition of 1.5 2^52, in whose lowest bits it then is
+        const double t = fma(z, 32 / LN2, 0x1.8p52), n = t - 0x1.8p52;
+        const int i = (int)(unsigned)__builtin_bit_cast(uint64_t, t);
+        const double r = fma(n, -LN2 / 32, z);     // (ln 2's own rounding: |z| 2^-54, below 2^-47)
+        double p = fma(r, 1.0 / 120, 1.0 / 24);
+        p = fma(r, p, 1.0 / 6);
+        p = fma(r, p, 0.5);
+        p = fma(r, p, 1.0);
+        p = fma(r, p, 1.0);
+        // times 2^(i / 32): the product is in 1 .. 2 and the result no smaller than 2^-159
+        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, table[i & 31] * p) + ((uint64_t)(int64_t)(i >> 5) << 52));
+    }
+};
+
 // What the rules of a row come to.
 struct Rule {
     double inv_t, min_p, top_p;          // min_p 0 and top_p 1: none
@@ -75,16 +112,24 @@ struct Rule {
     int top_k;                           // 0: none
     bool greedy;
 
+    const double* table;                 // of Exp
+
     // exp((l - max) / T) of a logit that may be kept
     __device__ __forceinline__ double weight(float l) const {
-        return l == top ? 1.0 : top == INFINITY ? 0.0 : exp(((double)l - (double)top) * inv_t);
+        return l == top ? 1.0 : top == INFINITY ? 0.0 : Exp{table}(((double)l - (double)top) * inv_t);
     }
 };
 
-__device__ __forceinline__ uint64_t fixed(double w) { return (uint64_t)(w * (double)(1ull << FRACTION) + 0.5); }
+// the nearest integer to w 2^43, w in 0 .. 1: the lowest bits of its sum with 2^52
+__device__ __forceinline__ uint64_t fixed(double w) {
+    return __builtin_bit_cast(uint64_t, fma(w, (double)(1ull << FRACTION), 0x1p52)) & ((1ull << 52) - 1);
+}
 
-__device__ __forceinline__ Rule rule_of(const SampleArgs& a, int row) {
+// (table: 32 numbers in LDS, filled here; a barrier follows)
+__device__ __forceinline__ Rule rule_of(const SampleArgs& a, int row, double* table) {
     Rule r;
+    Exp::fill(table);
+    r.table = table;
     const float t = a.temperature ? a.temperature[row] : 1.0f;
     r.greedy = !(t > 0.0f);
     r.inv_t = r.greedy ? 1.0 : 1.0 / (double)t;
@@ -100,23 +145,54 @@ __device__ __forceinline__ float logit(const uint8_t* row, int i) {
     return DT == F16 ? (float)reinterpret_cast<const _Float16*>(row)[i] : reinterpret_cast<const float*>(row)[i];
 }
 
+// The lane's value from the one that CTRL selects, 0 where there is none or the row is outside ROW_MASK (a shuffle through LDS
+// takes ten times as long, and these sums wait for each other).
+template <int CTRL, int ROW_MASK = 0xf>
+__device__ __forceinline__ unsigned moved(unsigned v) {
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xf, false);
+}
+template <int CTRL, int ROW_MASK = 0xf>
+__device__ __forceinline__ u64 moved(u64 v) {
+    return (u64)moved<CTRL, ROW_MASK>((unsigned)(v >> 32)) << 32 | moved<CTRL, ROW_MASK>((unsigned)v);
+}
+// sum over lanes 0 .. this one
+__device__ __forceinline__ u64 wave_scan(u64 v) {
+    v += moved<DPP_ROW_SHR1>(v);
+    v += moved<DPP_ROW_SHR1 + 1>(v);
+    v += moved<DPP_ROW_SHR1 + 3>(v);
+    v += moved<DPP_ROW_SHR1 + 7>(v);
+    v += moved<DPP_ROW_BCAST15, 0xA>(v);
+    v += moved<DPP_ROW_BCAST31, 0xC>(v);
+    return v;
+}
+__device__ __forceinline__ u64 last_lane(u64 v) {
+    return (u64)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), WAVE - 1) << 32 |
+           (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, WAVE - 1);
+}
+__device__ __forceinline__ u64 wave_sum(u64 v) { return last_lane(wave_scan(v)); }
+__device__ __forceinline__ unsigned wave_max(unsigned v) {
+    v = max(v, moved<DPP_ROW_SHR1>(v));
+    v = max(v, moved<DPP_ROW_SHR1 + 1>(v));
+    v = max(v, moved<DPP_ROW_SHR1 + 3>(v));
+    v = max(v, moved<DPP_ROW_SHR1 + 7>(v));
+    v = max(v, moved<DPP_ROW_BCAST15, 0xA>(v));
+    v = max(v, moved<DPP_ROW_BCAST31, 0xC>(v));
+    return (unsigned)__builtin_amdgcn_readlane((int)v, WAVE - 1);
+}
+
 // Sums of a value over the threads before this one, and over all.
-template <typename T>
-__device__ T before_and_total(T v, T* lds, T& total) {
-    T incl = v;
-#pragma unroll
-    for (int o = 1; o < WAVE; o *= 2) {
-        const T up = __shfl_up(incl, o);
-        if ((int)(threadIdx.x % WAVE) >= o) incl += up;
-    }
+__device__ __forceinline__ u64 before_and_total(u64 v, u64* lds, u64& total) {
+    const u64 incl = wave_scan(v);
     __syncthreads();
     if (threadIdx.x % WAVE == WAVE - 1) lds[threadIdx.x / WAVE] = incl;
     __syncthreads();
-    T base = 0;
+    u64 base = 0;
     total = 0;
+#pragma unroll
     for (int w = 0; w < ST / WAVE; ++w) {
-        if (w < (int)threadIdx.x / WAVE) base += lds[w];
-        total += lds[w];
+        const u64 sum = lds[w];
+        if (w < (int)threadIdx.x / WAVE) base += sum;
+        total += sum;
     }
     return base + incl - v;
 }
@@ -193,7 +269,7 @@ __device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* m
     int equal = 0;
     for (int i = lo; i < hi; ++i) equal += order_key(logit<DT>(l, i)) == key;
     u64 total;
-    const int64_t equal_before = (int64_t)before_and_total<u64>(equal, scan, total);
+    const int64_t equal_before = (int64_t)before_and_total(equal, scan, total);
     u64 sum = 0, n = 0;
     int64_t rank = equal_before;
     for (int i = lo; i < hi; ++i) {
@@ -203,9 +279,9 @@ __device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* m
         const double w = rule.weight(x);
         if (w >= rule.min_p) sum += fixed(w), ++n;
     }
-    const u64 before = before_and_total<u64>(sum, scan, total);
+    const u64 before = before_and_total(sum, scan, total);
     u64 all_kept;
-    before_and_total<u64>(n, scan, all_kept);
+    before_and_total(n, scan, all_kept);
     const float u = a.u[row];
     u64 target = u > 0.0f ? (u64)((double)u * (double)total) : 0;
     if (u >= 1.0f || target >= total) target = total - 1;
@@ -230,18 +306,23 @@ __device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* m
 
 // ---- a row by many workgroups --------------------------------------------------------
 //
-// The logits' bytes would take a microsecond or two; what there is to do is to keep a row's pieces busy at the same time,
-// and to read them few times.  Four launches, a workgroup to each chunk of a row but in the last:
-//   k_sample_top     the largest and smallest logit of the chunk
-//   k_sample_count   with the row's largest known: the chunk's part of a histogram of the distance to it (counts for top-k,
-//                    sums of weights for top-p); without either rule the sum of its weights
-//   k_sample_list    from the histogram the bins in which the border of top-k and of top-p can lie: sums over the tokens
-//                    above them, and a list of the tokens in them (left out where no row has either rule)
-//   k_sample_pick    a workgroup to each row: sorts the list, finds the border and the token.  (As a part of the launch before,
-//                    by the row's last workgroup, it took 26 us instead of 5 and 64 rows 108: that needs fences between the
-//                    dies, which write back and drop whole caches.)
+// The logits' bytes would take a microsecond or two (64 rows of 151003 in f16: 3.9); what there is to do is to keep a row's
+// pieces busy at the same time, and to read them few times.  Four launches, a workgroup to each chunk of a row but in the
+// last; us for 64 x 151003 f16 with rules of every kind, for 48 x 50007 float32 with top-p and for 1 x 128000 with top-k:
+//   k_sample_top     the largest and smallest logit of the chunk                                              9.8   5.8   3.7
+//   k_sample_count   with the row's largest known: the chunk's part of a histogram of the distance to it
+//                    (counts for top-k, sums of weights for top-p); without either rule the sum of its
+//                    weights                                                                                 19.5  11.9   5.9
+//   k_sample_list    from the histogram the bins in which the border of top-k and of top-p can lie: sums
+//                    over the tokens above them, and a list of the tokens in them (left out where no row
+//                    has either rule)                                                                        18.7  14.2   6.9
+//   k_sample_pick    a workgroup to each row: sorts the list, finds the border and the token                 13.7  10.9   8.1
+// The whole call: 60.8, 40.8 and 24.1 us.  A dependent launch costs some 4 us here; what is left are the chains of sums in
+// each, weights in 64 bits and additions to LDS, not bytes.  (A row's last workgroup doing the pick in the launch before
+// needs fences between the dies, which write back and drop whole caches: 26 us in place of 13 for one row, 108 for 64.)
 // Sums are integers, so that neither their order nor that of the list matters.  A row whose border bins hold more than
-// LIST tokens (equal logits, or a border far below the others) is done by k_sample_pick alone, from the start.
+// LIST tokens (equal logits, or a border far below the others) is done by k_sample_pick alone, from the start: 0.5 to
+// 0.9 ms for 128000 logits, equal ones or normal ones of a tenth of the temperature beside one of -1e30.
 
 // 8 logits from i on; those past the row's end are -inf
 template <int DT>
@@ -262,17 +343,6 @@ __device__ __forceinline__ void load_logits(const uint8_t* row, int i, int vocab
 #pragma unroll
         for (int e = 0; e < EACH; ++e) v[e] = i + e < vocab ? logit<DT>(row, i + e) : -INFINITY;
     }
-}
-
-__device__ __forceinline__ unsigned wave_max(unsigned v) {
-#pragma unroll
-    for (int o = 1; o < WAVE; o *= 2) v = max(v, (unsigned)__shfl_xor((int)v, o));
-    return v;
-}
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-#pragma unroll
-    for (int o = 1; o < WAVE; o *= 2) v += __shfl_xor(v, o);
-    return v;
 }
 
 template <int DT>
@@ -385,7 +455,8 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     const int row = blockIdx.y, tid = threadIdx.x;
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     uint8_t* ws = a.ws + row * a.row_bytes;
-    Rule rule = rule_of(a, row);
+    __shared__ double s_exp[32];
+    Rule rule = rule_of(a, row, s_exp);
     const Top t = row_top(a, ws, &s_top);
     if (t.most == 0 || rule.greedy) return;
     rule.top = key_logit(t.most);
@@ -422,7 +493,7 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
         for (int e = 0; e < EACH; ++e) {
             if (!order_key(v[e])) continue;
             const int b = bin.of(v[e]);
-            atomicAdd(&s_count[b], 1u);
+            if (by_count) atomicAdd(&s_count[b], 1u);
             if (by_mass) {
                 const u64 w = fixed(rule.weight(v[e]));
                 if (w) atomicAdd(&s_mass[b], w);
@@ -431,8 +502,7 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     }
     __syncthreads();
     for (int b = tid; b < BINS; b += ST) {
-        if (!s_count[b]) continue;
-        atomicAdd(reinterpret_cast<unsigned*>(ws + WS_COUNT) + b, s_count[b]);
+        if (s_count[b]) atomicAdd(reinterpret_cast<unsigned*>(ws + WS_COUNT) + b, s_count[b]);
         if (s_mass[b]) atomicAdd(reinterpret_cast<u64*>(ws + WS_MASS) + b, s_mass[b]);
     }
 }
@@ -450,6 +520,8 @@ __device__ __forceinline__ void find_bin(u64 want, u64 before, const u64* own, i
 
 template <int DT>
 __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
+    __shared__ u64 s_list[LIST];
+    __shared__ unsigned s_listed, s_first;
     __shared__ u64 scan[ST / WAVE];
     __shared__ u64 s_mass[MOST_BLOCKS];
     __shared__ unsigned s_kept[MOST_BLOCKS];
@@ -460,7 +532,8 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     uint8_t* ws = a.ws + row * a.row_bytes;
     RowState* state = reinterpret_cast<RowState*>(ws + WS_STATE);
-    Rule rule = rule_of(a, row);
+    __shared__ double s_exp[32];
+    Rule rule = rule_of(a, row, s_exp);
     if (rule.greedy || (rule.top_k == 0 && rule.top_p >= 1.0)) return;
     const Top t = row_top(a, ws, &s_top);
     rule.top = key_logit(t.most);
@@ -480,7 +553,7 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
         m[e] = reinterpret_cast<const u64*>(ws + WS_MASS)[tid * (BINS / ST) + e];
         own_n += n[e], own_m += m[e];
     }
-    const u64 before_n = before_and_total<u64>(own_n, scan, all_n), before_m = before_and_total<u64>(own_m, scan, all_m);
+    const u64 before_n = before_and_total(own_n, scan, all_n), before_m = before_and_total(own_m, scan, all_m);
     if (tid < 3) s_bin[tid] = BINS;
     __syncthreads();
     if (by_count) find_bin((u64)rule.top_k, before_n, n, &s_bin[0]);
@@ -513,6 +586,7 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     const int border = by_mass ? p_lo : k_bin;           // bins before it are kept for certain
 
     for (int b = tid; b < MOST_BLOCKS; b += ST) s_mass[b] = 0, s_kept[b] = 0;
+    if (tid == 0) s_listed = 0;
     __syncthreads();
     const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
     for (int base = from, block = 0; base < to; base += BLOCK, ++block) {
@@ -531,17 +605,15 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
                 in_list |= 1u << e;
             }
         }
-        // one place in the list's count for a wave's tokens: each addition to it waits for the one before
         if (__any(in_list != 0)) {
             const int mine = __popc(in_list), incl = wave_incl_scan(mine);
             unsigned at = 0;
-            if (tid % WAVE == WAVE - 1) at = atomicAdd(&state->listed, (unsigned)incl);
+            if (tid % WAVE == WAVE - 1) at = atomicAdd(&s_listed, (unsigned)incl);
             at = __shfl(at, WAVE - 1) + incl - mine;
 #pragma unroll
             for (int e = 0; e < EACH; ++e) {
                 if (!(in_list >> e & 1)) continue;
-                if (at < LIST)
-                    reinterpret_cast<u64*>(ws + WS_LIST)[at] = (u64)order_key(v[e]) << 32 | ~(unsigned)(base + tid * EACH + e);
+                if (at < LIST) s_list[at] = (u64)order_key(v[e]) << 32 | ~(unsigned)(base + tid * EACH + e);
                 ++at;
             }
         }
@@ -549,6 +621,12 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     }
     __syncthreads();
     store_blocks(a, ws, s_mass, s_kept);
+    // one addition to the row's count for all of the workgroup's tokens: each waits for the one before (with one for every
+    // wave and step 48 rows of 50007 took 16 us here)
+    if (s_listed == 0) return;
+    if (tid == 0) s_first = atomicAdd(&state->listed, s_listed);
+    __syncthreads();
+    for (unsigned i = tid; i < s_listed && s_first + i < LIST; i += ST) reinterpret_cast<u64*>(ws + WS_LIST)[s_first + i] = s_list[i];
 }
 
 // The token of a row: a workgroup each.
@@ -565,7 +643,8 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     const uint8_t* ws = a.ws + row * a.row_bytes;
     const RowState state = *reinterpret_cast<const RowState*>(ws + WS_STATE);
-    Rule rule = rule_of(a, row);
+    __shared__ double s_exp[32];
+    Rule rule = rule_of(a, row, s_exp);
     const Top t = row_top(a, ws, &s_top);
     if (t.most == 0 || rule.greedy) {
         if (tid == 0) {
@@ -635,7 +714,7 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
         }
         // tokens of the list before those of k_bin, and how many of the list top-k leaves
         u64 n_k;
-        before_and_total<u64>((u64)of_k, scan, n_k);
+        before_and_total((u64)of_k, scan, n_k);
         const int begin_k = (int)listed - (int)n_k;
         const int by_k = by_count ? begin_k + (int)((u64)rule.top_k - k_before) : (int)listed;
         int keep = by_k;
@@ -647,8 +726,8 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
                 own += w[e];
                 if (i >= begin_k) own_k += w[e];
             }
-            before_and_total<u64>(own_k, scan, in_k);
-            const u64 before = p_before + before_and_total<u64>(own, scan, all);
+            before_and_total(own_k, scan, in_k);
+            const u64 before = p_before + before_and_total(own, scan, all);
             const double p = ceil(rule.top_p * (double)(mass_lo + in_k));
             const u64 want = p > 1.0 ? (u64)p : 1;
             // (past p_hi there are tokens that the list leaves out, but the sum has reached `want` before)
@@ -661,7 +740,7 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
                 run += w[e];
             }
             u64 total_n;
-            before_and_total<u64>((u64)n, scan, total_n);
+            before_and_total((u64)n, scan, total_n);
             keep = (int)total_n;
         }
         const u64 last = s_list[max(keep, 1) - 1];
@@ -679,8 +758,8 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     // the block that the random number falls into
     u64 total, kept;
     const u64 mine = tid < a.blocks ? s_mass[tid] : 0;
-    const u64 before = before_and_total<u64>(mine, scan, total);
-    before_and_total<u64>(tid < a.blocks ? (u64)s_kept[tid] : 0ull, scan, kept);
+    const u64 before = before_and_total(mine, scan, total);
+    before_and_total(tid < a.blocks ? (u64)s_kept[tid] : 0ull, scan, kept);
     const float u = a.u[row];
     u64 target = u > 0.0f ? (u64)((double)u * (double)total) : 0;
     if (u >= 1.0f || target >= total) target = total - 1;
@@ -702,7 +781,7 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
         }
         sum += w[e];
     }
-    u64 at = s_sum + before_and_total<u64>(sum, scan, in_block);
+    u64 at = s_sum + before_and_total(sum, scan, in_block);
     if (target < at || target >= at + sum) return;
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
