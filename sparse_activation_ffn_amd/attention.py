@@ -15,7 +15,7 @@ import torch
 
 from . import binding as pb
 from .layer import DeviceLayer, StepBuffers, decode_step
-from .mx import MxBuffer, MxLinear
+from .mx import MxBuffer, MxLinear, Scratch
 
 
 class PagedCache:
@@ -97,7 +97,7 @@ class AttentionLayer:
         self.head_dim = w_qkv.shape[0] // (q_heads + 2 * kv_heads)
         self.w_qkv, self.w_o, self.rope = w_qkv, w_o, rope
         self.rule = rule or pb.make_score_rule(1.0 / math.sqrt(self.head_dim))
-        self.ws: Optional[torch.Tensor] = None
+        self.ws = Scratch()
 
     def heads(self, x: Union[torch.Tensor, pb.Mx], dtype=None):
         """Queries, keys and values of x [tokens][d] (microscaled: for an MxLinear w_qkv, and the
@@ -111,9 +111,7 @@ class AttentionLayer:
         q, k, v = self.heads(x, cache.k.dtype)
         pb.pi_rope_append(cache.cache, layer, batch, self.rope, q, q, k, v)
         need = pb.pi_attention_workspace_bytes(cache.cache, batch, self.q_heads)
-        if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        pb.pi_paged_attention(cache.cache, layer, batch, self.rule, q, q, None, self.ws)
+        pb.pi_paged_attention(cache.cache, layer, batch, self.rule, q, q, None, self.ws.bytes(need, q.device))
         if isinstance(self.w_o, MxLinear):
             return self.w_o(q.flatten(1))                # (a view: the heads of a row lie side by side)
         return q.reshape(q.shape[0], self.q_heads * self.head_dim) @ self.w_o.t()

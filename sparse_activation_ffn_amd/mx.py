@@ -12,28 +12,41 @@ import torch
 from . import binding as pb
 
 
+class Scratch:
+    """Device memory that the calls of one stream use in turn.  For one that needs more there is a
+    new piece, a power of two of bytes; the pieces before stay, since a captured graph may name
+    them (all together are less than twice the last)."""
+
+    def __init__(self):
+        self.pieces = []
+
+    def bytes(self, need: int, device) -> torch.Tensor:
+        if not self.pieces or self.pieces[-1].numel() < need:
+            self.pieces.append(torch.empty(max(256, 1 << (need - 1).bit_length()), dtype=torch.uint8, device=device))
+        return self.pieces[-1]
+
+
 class MxBuffer:
     """Activations of up to as many rows as any call had, cols wide, in 8 bits: one step's after
     the other (calls that may overlap, on different streams, need one each)."""
 
     def __init__(self, cols: int, fmt: int = pb.PI_MXFP8):
         self.cols, self.fmt = cols, fmt
-        self.codes = self.scales = self.mx = None
+        self.codes, self.scales = Scratch(), Scratch()
+        self.mx: Optional[pb.Mx] = None
 
     def rows(self, n: int, device) -> pb.Mx:
-        if self.mx is not None and self.mx.rows == n:
-            return self.mx
-        if self.codes is None or self.codes.shape[0] < n:
-            u8 = dict(dtype=torch.uint8, device=device)
-            self.codes = torch.empty((n, self.cols // 2 if self.fmt == pb.PI_MXFP4 else self.cols), **u8)
-            self.scales = torch.empty((n, self.cols // 32), **u8)
-        self.mx = pb.make_mx(self.codes[:n], self.scales[:n], self.fmt)
+        if self.mx is None or self.mx.rows != n:
+            parts = [p.bytes(n * width, device)[:n * width].view(n, width) for p, width in
+                     ((self.codes, self.cols // 2 if self.fmt == pb.PI_MXFP4 else self.cols), (self.scales, self.cols // 32))]
+            self.mx = pb.make_mx(*parts, self.fmt)
         return self.mx
 
 
 class MxLinear:
     """y = x W^T + bias with W [n][d] (float16 or float32 device tensor, d a multiple of 32) kept in
-    MXFP4; bias float32 [n] or None."""
+    MXFP4; bias float32 [n] or None.  Its buffers are those of one stream: calls that may overlap
+    need an MxLinear each."""
 
     def __init__(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None):
         n, d = weight.shape
@@ -41,7 +54,7 @@ class MxLinear:
         self.weight = pb.empty_mx(n, d, pb.PI_MXFP4, weight.device)
         pb.pi_mx_quantize(weight, self.weight)
         self.input = MxBuffer(d)
-        self.ws: Optional[torch.Tensor] = None
+        self.ws = Scratch()
 
     def __call__(self, x: Union[torch.Tensor, pb.Mx], dtype=None) -> torch.Tensor:
         """x [tokens][d]: float16 or float32 (rows may be strided; quantised to 8 bits here), or
@@ -54,10 +67,9 @@ class MxLinear:
             pb.pi_mx_quantize(x, a)
         n, d = self.shape
         need = pb.pi_mx_product_workspace_bytes(a.rows, n, d)
-        if need and (self.ws is None or self.ws.numel() < need):
-            self.ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = self.ws.bytes(need, device) if need else None
         out = torch.empty((a.rows, n), dtype=dtype, device=device)
-        pb.pi_mx_product(a, self.weight, out, bias=self.bias, ws=self.ws)
+        pb.pi_mx_product(a, self.weight, out, bias=self.bias, ws=ws)
         return out
 
 
@@ -67,7 +79,7 @@ class TokenHead:
 
     def __init__(self, norm_weight: torch.Tensor, vocabulary: MxLinear, eps: float = 1e-5):
         self.norm, self.vocabulary = pb.make_norm(norm_weight, eps), vocabulary
-        self.ws: Optional[torch.Tensor] = None
+        self.ws = Scratch()
 
     def logits(self, x: torch.Tensor, delta: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Of x + delta (delta: what the last layer has yet to add, see DecoderLayer.step)."""
@@ -81,8 +93,6 @@ class TokenHead:
         logits = self.logits(x, delta)
         rows, vocab = logits.shape
         need = pb.pi_sample_workspace_bytes(rows, vocab)
-        if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=x.device)
         token = torch.empty(rows, dtype=torch.int32, device=x.device)
-        pb.pi_sample(logits, rule or pb.make_sample_rule(), u, token, ws=self.ws)
+        pb.pi_sample(logits, rule or pb.make_sample_rule(), u, token, ws=self.ws.bytes(need, x.device))
         return token

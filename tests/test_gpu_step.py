@@ -191,3 +191,32 @@ def test_a_step_in_a_graph():
         assert torch.equal(got, step())
         randn(1000, 1000) @ randn(1000, 1000)
         torch.cuda.synchronize()
+
+
+def test_a_graph_keeps_its_buffers():
+    """A captured step gives the same after calls with many more rows, and after their memory's neighbours were written."""
+    randn = gen(10)
+    lin = MxLinear((randn(2048, 2048) / 45).half())
+    head = TokenHead((1 + 0.1 * randn(2048)).half(), MxLinear((randn(1003, 2048) / 4).half()))
+    x, u = randn(20, 2048).half(), torch.rand(20, device=DEV)
+
+    def step():
+        y = lin(x)
+        return y, head(y, u, pb.make_sample_rule())
+    want = [t.clone() for t in step()]                               # (20 rows: K is split, with a workspace)
+    assert lin.ws.pieces and lin.input.codes.pieces and head.ws.pieces
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    named = [p.data_ptr() for s in (lin.ws, lin.input.codes, lin.input.scales, head.ws, head.vocabulary.input.codes) for p in s.pieces]
+    for rows in (40, 64, 1000):
+        head(lin(randn(rows, 2048).half()), torch.rand(rows, device=DEV))
+    torch.cuda.synchronize()
+    # what a freed piece would be given to
+    fill = [torch.full((1 << size,), 255, dtype=torch.uint8, device=DEV) for size in range(8, 24) for _ in range(4)]
+    assert not {t.data_ptr() for t in fill} & set(named)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

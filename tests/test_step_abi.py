@@ -166,3 +166,21 @@ def test_binding_refuses_wrong_shapes():
         pb.pi_mx_product(mx, wm, torch.zeros((4, 10)), bias=torch.zeros(9))
     with pytest.raises(ValueError):
         pb.make_sample_rule(top_k=torch.zeros(3))
+
+
+def test_buffers_that_graphs_may_name_stay():
+    """Growing buffers hand out a part of one piece, keep the pieces before it, and use less than twice the last."""
+    from sparse_activation_ffn_amd.mx import MxBuffer, Scratch
+    s, seen = Scratch(), []
+    for need in (1, 300, 256, 5000, 4097, 70000, 3):
+        t = s.bytes(need, "cpu")
+        assert t.numel() >= need
+        seen.append(t)
+    assert {t.data_ptr() for t in seen} == {t.data_ptr() for t in s.pieces} and seen[-1] is s.pieces[-1]
+    assert sum(t.numel() for t in s.pieces) < 2 * s.pieces[-1].numel()
+    for fmt, width in ((pb.PI_MXFP8, 96), (pb.PI_MXFP4, 48)):
+        b = MxBuffer(96, fmt)
+        for n in (0, 3, 1, 200, 3):
+            m = b.rows(n, "cpu")
+            assert (m.rows, m.cols, m.format) == (n, 96, fmt) and m is b.rows(n, "cpu")
+            assert tuple(m._keep[0].shape) == (n, width) and tuple(m._keep[1].shape) == (n, 3)
