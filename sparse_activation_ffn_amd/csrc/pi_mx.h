@@ -28,6 +28,17 @@ inline pi_status check_mx(const pi_mx* m, const char* name) {
     return PI_OK;
 }
 
+// Whether spans of bytes lie apart (one that is NULL does)
+inline bool apart(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return !a || !b || x + (uint64_t)bytes_a <= y || y + (uint64_t)bytes_b <= x;
+}
+
+inline bool apart(const void* p, int64_t bytes, const pi_mx* m) {
+    return apart(p, bytes, m->codes, m->rows * mx_row_bytes(m->format, m->cols)) &&
+           apart(p, bytes, m->scales, (int64_t)m->rows * (m->cols / 32));
+}
+
 inline pi_status check_elem_dtype(int dtype, const char* name) {
     CHECK(dtype == PI_F32 || dtype == PI_F16, PI_ERR_DTYPE, "%s: dtype must be PI_F32 or PI_F16", name);
     return PI_OK;

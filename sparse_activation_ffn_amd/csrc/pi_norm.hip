@@ -398,6 +398,7 @@ pi_status check_matrix(const void* data, int64_t stride, int dtype, const pi_mx*
     CHECK(aligned(data, dtype_size(dtype)), PI_ERR_ALIGN, "%s must be aligned to its elements", name);
     CHECK(stride >= (out && mx->rows > 1 ? mx->cols : 0) && stride < ((int64_t)1 << 40), PI_ERR_SHAPE,
           "%s: row_stride must be in %s..2^40", name, out ? "cols" : "0");
+    CHECK(apart(data, ((mx->rows - 1) * stride + mx->cols) * dtype_size(dtype), mx), PI_ERR_ARG, "%s and mx overlap", name);
     return PI_OK;
 }
 
@@ -440,6 +441,23 @@ pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, 
     return PI_OK;
 }
 
+// an output that begins where an input does takes its place: the same rows, of the same type
+pi_status check_in_place(const pi_rows* out, const char* name, int dtype, const pi_rows* in, int in_dtype, int tokens, int heads) {
+    if (!out || !in || out->data != in->data) return PI_OK;
+    CHECK(dtype == in_dtype && (tokens == 1 || out->token_stride == in->token_stride) &&
+              (heads == 1 || out->head_stride == in->head_stride),
+          PI_ERR_ARG, "norm: %s takes an input's place with other rows or another type", name);
+    return PI_OK;
+}
+
+// a matrix in a microscaled format takes no input's or output's place
+pi_status check_apart(const pi_rows* r, const char* name, int dtype, const pi_mx* mx, int d, int tokens, int heads) {
+    if (!r || !mx) return PI_OK;
+    const int64_t last = (tokens - 1) * r->token_stride + (heads - 1) * r->head_stride;
+    CHECK(apart(r->data, (last + d) * dtype_size(dtype), mx), PI_ERR_ARG, "norm: %s and mx overlap", name);
+    return PI_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -451,6 +469,8 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
     CHECK(norm->eps >= 0.0f && std::isfinite(norm->eps), PI_ERR_ARG, "norm: eps must be finite and not negative");
     CHECK(tokens >= 0 && heads >= 1 && (int64_t)tokens * heads <= (1 << 23), PI_ERR_SHAPE,
           "norm: heads must be >= 1 and tokens * heads in 0..2^23");
+    // (a workgroup to a row: a launch holds fewer than 2^32 threads)
+    CHECK(norm->d <= 2048 || (int64_t)tokens * heads <= (1 << 21), PI_ERR_SHAPE, "norm: tokens * heads must be in 0..2^21 for d > 2048");
     TRY(check_elem_dtype(dtype, "norm"));
     const int d = norm->d;
     bool vec = d % 8 == 0;
@@ -489,6 +509,14 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
         a.y = (uint8_t*)y->data, a.y_ts = y->token_stride * size, a.y_hs = y->head_stride * size;
         CHECK(!sum || sum->data != y->data, PI_ERR_ARG, "norm: sum and y must differ");
     }
+    for (const pi_rows* out : {sum, y}) {
+        const char* name = out == sum ? "sum" : "y";
+        TRY(check_in_place(out, name, dtype, x, dtype, tokens, heads));
+        TRY(check_in_place(out, name, dtype, delta, ddtype, tokens, heads));
+        TRY(check_apart(out, name, dtype, mx, d, tokens, heads));
+    }
+    TRY(check_apart(x, "x", dtype, mx, d, tokens, heads));
+    TRY(check_apart(delta, "delta", ddtype, mx, d, tokens, heads));
     if (mx) a.format = mx->format, a.codes = (uint8_t*)mx->codes, a.scales = mx->scales;
     if (norm->weight) a.wdtype = norm->wdtype, a.weight = (const uint8_t*)norm->weight;
     a.eps = norm->eps;

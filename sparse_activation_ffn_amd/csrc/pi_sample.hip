@@ -838,6 +838,15 @@ pi_status pi_sample(const void* logits, int32_t rows, int32_t vocab, int64_t row
     CHECK(ws && ws_bytes >= sample_bytes(rows, vocab), PI_ERR_WORKSPACE, "sample: workspace of %zu bytes, %zu needed", ws_bytes,
           sample_bytes(rows, vocab));
     CHECK(aligned(ws, 256), PI_ERR_ALIGN, "sample: workspace must be 256-byte aligned");
+    const int64_t list = (int64_t)rows * 4, span = ((rows - 1) * row_stride + vocab) * dtype_size(dtype);
+    const void* outs[] = {token, prob, kept};
+    const void* ins[] = {u, rule->temperature, rule->top_k, rule->top_p, rule->min_p};
+    for (int i = 0; i < 3; ++i) {
+        bool free = apart(outs[i], list, logits, span) && apart(outs[i], list, ws, sample_bytes(rows, vocab)) &&
+                    apart(outs[i], list, outs[(i + 1) % 3], list);
+        for (const void* in : ins) free = free && apart(outs[i], list, in, list);
+        CHECK(free, PI_ERR_ARG, "sample: token, prob and kept may overlap neither each other nor what the call reads");
+    }
     SampleArgs a{(const uint8_t*)logits, row_stride, rule->temperature, rule->top_k, rule->top_p, rule->min_p, u, token, prob,
                  kept, rows, vocab, 0, 0, 0, (uint8_t*)ws, WS_ROW};
     chunks_of(a);

@@ -184,3 +184,41 @@ def test_buffers_that_graphs_may_name_stay():
             m = b.rows(n, "cpu")
             assert (m.rows, m.cols, m.format) == (n, 96, fmt) and m is b.rows(n, "cpu")
             assert tuple(m._keep[0].shape) == (n, width) and tuple(m._keep[1].shape) == (n, 3)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=1 << 21, heads=2, d=2056), pb.PI_ERR_SHAPE), (dict(tokens=(1 << 21) + 1, d=8192), pb.PI_ERR_SHAPE),
+    # an input's place with other rows or another type
+    (dict(x=_rows(token_stride=256), y=_rows()), pb.PI_ERR_ARG), (dict(x=_rows(head_stride=256), y=_rows(), heads=2), pb.PI_ERR_ARG),
+    (dict(delta=_rows(FAKE << 4), ddtype=pb.PI_F32), pb.PI_ERR_ARG),
+    (dict(delta=_rows(FAKE << 8), sum_out=_rows(FAKE << 8, 256)), pb.PI_ERR_ARG),
+    # a microscaled output of 4 x 128 codes and 4 x 4 scales
+    (dict(mx=_mx(scales=FAKE << 8)), pb.PI_ERR_ARG), (dict(mx=_mx(codes=FAKE << 8, scales=FAKE + 1008)), pb.PI_ERR_ARG),
+    (dict(mx=_mx(codes=(FAKE << 4) - 496, scales=FAKE << 8)), pb.PI_ERR_ARG),
+    (dict(mx=_mx(codes=FAKE << 6, scales=FAKE << 8), delta=_rows((FAKE << 8) - 1008)), pb.PI_ERR_ARG)])
+def test_norm_refuses_rows_and_overlaps(L, kw, status):
+    assert _norm(L, **kw) == status
+
+
+def test_refusals_of_overlaps(L):
+    far = FAKE << 8
+    m = _mx(codes=far, scales=far << 2)                               # 4 x 128: x takes 1024 bytes of f16
+    for x in (far, far + 510, far - 1022, far << 2, (far << 2) + 14, (far << 2) - 1022):
+        assert L.pi_mx_quantize(x, 128, pb.PI_F16, ref(m), None) == pb.PI_ERR_ARG
+        assert L.pi_mx_dequantize(ref(m), x, 128, pb.PI_F16, None) == pb.PI_ERR_ARG
+    w = _mx(format=pb.PI_MXFP4, rows=256, codes=far << 4, scales=far << 6)
+    for out in (far, far << 2, far << 4, far << 6, far << 8, (far << 8) + 1020):
+        assert L.pi_mx_product(ref(m), ref(w), far << 8, out, 256, pb.PI_F16, None, 0, None) == pb.PI_ERR_ARG
+    need = L.pi_mx_product_workspace_bytes(48, 256, 8192)
+    assert need
+    m, w = _mx(rows=48, cols=8192), _mx(format=pb.PI_MXFP4, rows=256, cols=8192)
+    assert L.pi_mx_product(ref(m), ref(w), None, far + need - 4, 256, pb.PI_F16, far, need, None) == pb.PI_ERR_ARG
+    need = L.pi_sample_workspace_bytes(2, 1000)
+    at = [far * i for i in range(1, 11)]                              # logits, four lists, u, token, prob, kept, workspace
+
+    def call(token, prob, kept):
+        rule = pb.SampleRule(*at[1:5])
+        return L.pi_sample(at[0], 2, 1000, 1000, pb.PI_F16, ref(rule), at[5], token, prob, kept, at[9], need, None)
+    for i in (0, 1, 2, 3, 4, 5, 9):
+        assert call(at[i], at[7], at[8]) == call(at[6], at[i] + 4, at[8]) == call(at[6], None, at[i]) == pb.PI_ERR_ARG
+    assert call(at[6], at[6] + 4, None) == call(at[6], None, at[6]) == call(at[6], at[7], at[7] - 4) == pb.PI_ERR_ARG
