@@ -68,42 +68,30 @@ __device__ __forceinline__ float key_logit(unsigned key) {
     return __builtin_bit_cast(float, key >> 31 ? key & 0x7fffffffu : ~key);
 }
 
-// exp for z <= 0 by a table of 2^(j/32) (Tang, ACM TOMS 15(2), 1989): z = (32 m + j) ln 2 / 32 + r with |r| <= ln 2 / 64, exp(z)
-// = 2^m 2^(j/32) exp(r), exp(r) by its series to r^5 (the next term is 2^-49).  Weights are needed to 2^-44; the library's
-// function takes three times the operations, and a row's distribution hundreds of thousands of them.
-__constant__ double EXP2_32[32] = {
-    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
-    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
-    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
-    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
-    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
-    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
-    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
-    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
-
+// exp for z <= 0 by a table of 2^(j/128) (Tang, ACM TOMS 15(2), 1989): z = (128 m + j) ln 2 / 128 + r with |r| <= ln 2 / 256,
+// exp(z) = 2^m 2^(j/128) exp(r), exp(r) by its series to r^4 (the next term is 2^-49).  Weights are needed to 2^-44; the
+// library's function takes three times the operations, and a row's distribution hundreds of thousands of them.
 constexpr double LN2 = 0.693147180559945309417;
+constexpr int EXPS = 128;
 
-struct Exp {
-    const double* table;                 // in LDS
-    // the whole workgroup calls it, a barrier follows before the first use
-    static __device__ void fill(double* lds) {
-        if (threadIdx.x < 32) lds[threadIdx.x] = EXP2_32[threadIdx.x];
-    }
-    __device__ __forceinline__ double operator()(double z) const {
-        if (z < -110.0) return 0.0;      // (below the least float32, which min-p may be)
-        // the nearest integer by the addition of 1.5 2^52, in whose lowest bits it then is
-        const double t = fma(z, 32 / LN2, 0x1.8p52), n = t - 0x1.8p52;
-        const int i = (int)(unsigned)__builtin_bit_cast(uint64_t, t);
-        const double r = fma(n, -LN2 / 32, z);     // (ln 2's own rounding: |z| 2^-54, below 2^-47)
-        double p = fma(r, 1.0 / 120, 1.0 / 24);
-        p = fma(r, p, 1.0 / 6);
-        p = fma(r, p, 0.5);
-        p = fma(r, p, 1.0);
-        p = fma(r, p, 1.0);
-        // times 2^(i / 32): the product is in 1 .. 2 and the result no smaller than 2^-159
-        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, table[i & 31] * p) + ((uint64_t)(int64_t)(i >> 5) << 52));
-    }
-};
+// the table, by the whole workgroup; a barrier follows before the first use
+__device__ __forceinline__ void fill_exps(double* lds) {
+    if (threadIdx.x < EXPS) lds[threadIdx.x] = exp2((double)threadIdx.x / EXPS);
+}
+__device__ __forceinline__ double exp_by(const double* table, double z) {
+    z = fmax(z, -110.0);                 // (below the least float32, which min-p may be)
+    // the nearest integer by the addition of 1.5 2^52, in whose lowest bits it then is
+    const double t = fma(z, EXPS / LN2, 0x1.8p52), n = t - 0x1.8p52;
+    const int i = (int)(unsigned)__builtin_bit_cast(uint64_t, t);
+    const double r = fma(n, -LN2 / EXPS, z);           // (ln 2's own rounding: |z| 2^-54, below 2^-47)
+    double p = fma(r, 1.0 / 24, 1.0 / 6);
+    p = fma(r, p, 0.5);
+    p = fma(r, p, 1.0);
+    p = fma(r, p, 1.0);
+    // times 2^(i / 128): the product is in 1 .. 2 and the result no smaller than 2^-159
+    const uint64_t b = __builtin_bit_cast(uint64_t, table[i & (EXPS - 1)] * p);
+    return __builtin_bit_cast(double, (uint64_t)((unsigned)(b >> 32) + ((unsigned)(i >> 7) << 20)) << 32 | (unsigned)b);
+}
 
 // What the rules of a row come to.
 struct Rule {
@@ -112,11 +100,12 @@ struct Rule {
     int top_k;                           // 0: none
     bool greedy;
 
-    const double* table;                 // of Exp
+    const double* table;                 // of exp_by
 
     // exp((l - max) / T) of a logit that may be kept
     __device__ __forceinline__ double weight(float l) const {
-        return l == top ? 1.0 : top == INFINITY ? 0.0 : Exp{table}(((double)l - (double)top) * inv_t);
+        if (top == INFINITY) return l == top ? 1.0 : 0.0;
+        return exp_by(table, ((double)l - (double)top) * inv_t);
     }
 };
 
@@ -125,10 +114,10 @@ __device__ __forceinline__ uint64_t fixed(double w) {
     return __builtin_bit_cast(uint64_t, fma(w, (double)(1ull << FRACTION), 0x1p52)) & ((1ull << 52) - 1);
 }
 
-// (table: 32 numbers in LDS, filled here; a barrier follows)
+// (table: EXPS numbers in LDS, filled here; a barrier follows)
 __device__ __forceinline__ Rule rule_of(const SampleArgs& a, int row, double* table) {
     Rule r;
-    Exp::fill(table);
+    fill_exps(table);
     r.table = table;
     const float t = a.temperature ? a.temperature[row] : 1.0f;
     r.greedy = !(t > 0.0f);
@@ -195,6 +184,22 @@ __device__ __forceinline__ u64 before_and_total(u64 v, u64* lds, u64& total) {
         total += sum;
     }
     return base + incl - v;
+}
+
+// The same of two values, between the same two barriers (lds: 2 ST / WAVE).
+__device__ __forceinline__ void before_and_total(u64 v, u64 v2, u64* lds, u64& before, u64& before2, u64& total, u64& total2) {
+    const u64 incl = wave_scan(v), incl2 = wave_scan(v2);
+    __syncthreads();
+    if (threadIdx.x % WAVE == WAVE - 1) lds[threadIdx.x / WAVE] = incl, lds[ST / WAVE + threadIdx.x / WAVE] = incl2;
+    __syncthreads();
+    total = total2 = 0;
+    before = incl - v, before2 = incl2 - v2;
+#pragma unroll
+    for (int w = 0; w < ST / WAVE; ++w) {
+        const u64 sum = lds[w], sum2 = lds[ST / WAVE + w];
+        if (w < (int)threadIdx.x / WAVE) before += sum, before2 += sum2;
+        total += sum, total2 += sum2;
+    }
 }
 
 // A row by one workgroup, whatever it holds: the border of the kept set, in the order of the keys, is found digit by digit (8
@@ -309,48 +314,83 @@ __device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* m
 // The logits' bytes would take a microsecond or two (64 rows of 151003 in f16: 3.9); what there is to do is to keep a row's
 // pieces busy at the same time, and to read them few times.  Four launches, a workgroup to each chunk of a row but in the
 // last; us for 64 x 151003 f16 with rules of every kind, for 48 x 50007 float32 with top-p and for 1 x 128000 with top-k:
-//   k_sample_top     the largest and smallest logit of the chunk                                              9.8   5.8   3.7
+//   k_sample_top     the largest and smallest logit of the chunk                                              8.2   5.7   3.6
 //   k_sample_count   with the row's largest known: the chunk's part of a histogram of the distance to it
 //                    (counts for top-k, sums of weights for top-p); without either rule the sum of its
-//                    weights                                                                                 19.5  11.9   5.9
+//                    weights                                                                                 17.5   9.7   5.2
 //   k_sample_list    from the histogram the bins in which the border of top-k and of top-p can lie: sums
 //                    over the tokens above them, and a list of the tokens in them (left out where no row
-//                    has either rule)                                                                        18.7  14.2   6.9
-//   k_sample_pick    a workgroup to each row: sorts the list, finds the border and the token                 13.7  10.9   8.1
-// The whole call: 60.8, 40.8 and 24.1 us.  A dependent launch costs some 4 us here; what is left are the chains of sums in
-// each, weights in 64 bits and additions to LDS, not bytes.  (A row's last workgroup doing the pick in the launch before
+//                    has either rule)                                                                        17.8  13.2   5.8
+//   k_sample_pick    a workgroup to each row: sorts the list, finds the border and the token                 12.7   9.8   7.3
+// The whole call: 55.3, 36.4 and 21.5 us.  A dependent launch costs some 4 us here; what is left are the chains of sums in
+// each and weights in 64 bits (6 of k_sample_count's 17.5), neither bytes nor atomics.  (A row's last workgroup doing the pick in the launch before
 // needs fences between the dies, which write back and drop whole caches: 26 us in place of 13 for one row, 108 for 64.)
 // Sums are integers, so that neither their order nor that of the list matters.  A row whose border bins hold more than
 // LIST tokens (equal logits, or a border far below the others) is done by k_sample_pick alone, from the start: 0.5 to
 // 0.9 ms for 128000 logits, equal ones or normal ones of a tenth of the temperature beside one of -1e30.
 
-// 8 logits from i on; those past the row's end are -inf
+// 8 logits from i on, as they are stored; those past the row's end are -inf
 template <int DT>
-__device__ __forceinline__ void load_logits(const uint8_t* row, int i, int vocab, float* v) {
-    if (i + EACH <= vocab) {
-        if constexpr (DT == F16) {
+struct Logits {
+    u4 v[DT == F16 ? 1 : 2];
+    __device__ __forceinline__ void load(const uint8_t* row, int i, int vocab) {
+        if (i + EACH <= vocab) {
+            __builtin_memcpy(v, row + (int64_t)i * (DT == F16 ? 2 : 4), sizeof(v));
+        } else if constexpr (DT == F16) {
             h8 t;
-            __builtin_memcpy(&t, row + (int64_t)i * 2, 16);
 #pragma unroll
-            for (int e = 0; e < EACH; ++e) v[e] = (float)t[e];
+            for (int e = 0; e < EACH; ++e) t[e] = i + e < vocab ? reinterpret_cast<const _Float16*>(row)[i + e] : (_Float16)-INFINITY;
+            v[0] = __builtin_bit_cast(u4, t);
         } else {
-            f4 t[2];
-            __builtin_memcpy(t, row + (int64_t)i * 4, 32);
 #pragma unroll
-            for (int e = 0; e < EACH; ++e) v[e] = t[e / 4][e % 4];
+            for (int e = 0; e < EACH; ++e) v[e / 4][e % 4] = __builtin_bit_cast(unsigned, i + e < vocab ? logit<DT>(row, i + e) : -INFINITY);
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < EACH; ++e) v[e] = i + e < vocab ? logit<DT>(row, i + e) : -INFINITY;
     }
-}
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (DT == F32) return bits_f(v[e / 4][e % 4]);
+        return e % 2 ? half_hi(v[0][e / 2]) : half_lo(v[0][e / 2]);
+    }
+};
+
+// A workgroup's logits, BLOCK by BLOCK: STEPS of them are loaded at once, the first before all else that a kernel does, and
+// the next while these are worked on (one after the other each took 2 us: 64 x 151003, five to a chunk).
+template <int DT>
+struct Chunk {
+    static constexpr int STEPS = DT == F16 ? 4 : 2;      // (registers for two workgroups on a unit)
+    const uint8_t* row;
+    int from, to, vocab;
+    Logits<DT> next[STEPS];
+    __device__ __forceinline__ Chunk(const SampleArgs& a)
+        : row(a.logits + blockIdx.y * a.stride * (DT == F16 ? 2 : 4)), from(blockIdx.x * a.chunk),
+          to(min(from + a.chunk, a.vocab)), vocab(a.vocab) {}
+    __device__ __forceinline__ void load(int base) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            if (base + s * BLOCK < to) next[s].load(row, base + s * BLOCK + threadIdx.x * EACH, vocab);
+    }
+    // f(logits, index of the thread's first, number of the block in the chunk)
+    template <class F>
+    __device__ __forceinline__ void each(F f) {
+#pragma unroll 1
+        for (int base = from, block = 0; base < to; base += STEPS * BLOCK, block += STEPS) {
+            Logits<DT> now[STEPS];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) now[s] = next[s];
+            load(base + STEPS * BLOCK);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                if (base + s * BLOCK < to) f(now[s], base + s * BLOCK + (int)threadIdx.x * EACH, block + s);
+        }
+    }
+};
 
 template <int DT>
 __global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
     __shared__ unsigned s_most[ST / WAVE], s_least[ST / WAVE], s_at[ST / WAVE];
     __shared__ int s_count[ST / WAVE];
     const int row = blockIdx.y, tid = threadIdx.x, wave = tid / WAVE;
-    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
+    Chunk<DT> chunk(a);
+    chunk.load(chunk.from);
     uint8_t* ws = a.ws + row * a.row_bytes;
     // what the later launches add to
     for (int b = blockIdx.x * ST + tid; b < BINS; b += gridDim.x * ST) {
@@ -359,26 +399,32 @@ __global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
     }
     if (blockIdx.x == 0 && tid == 0) reinterpret_cast<RowState*>(ws + WS_STATE)->listed = 0;
 
-    // the smallest key as the largest of the complements
-    unsigned most = 0, low = 0, at = 0;
-    int count = 0;
-    const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
-    for (int i = from + tid * EACH; i < to; i += ST * EACH) {
-        float v[EACH];
-        load_logits<DT>(l, i, a.vocab, v);
+    // the largest, smallest and number of those that may be kept; `best` holds the largest first
+    float most = -INFINITY, least = INFINITY;
+    int count = 0, best_at = 0;                // (count: of the whole wave)
+    Logits<DT> best{};
+    chunk.each([&](const Logits<DT>& v, int i, int) __attribute__((always_inline)) {
+        float m = -INFINITY;
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const unsigned key = order_key(v[e]);
-            if (key > most) most = key, at = i + e;
-            low = max(low, key ? ~key : 0u);
-            count += key != 0;
+            const bool may = v[e] > -INFINITY;
+            count += __popcll(__ballot(may));
+            m = fmaxf(m, v[e]);                // (the other one of a NaN)
+            least = fminf(least, may ? v[e] : INFINITY);
         }
-    }
-    const unsigned top = wave_max(most);
+        if (m > most) most = m, best = v, best_at = i;
+    });
+    unsigned at = 0;
+#pragma unroll
+    for (int e = EACH - 1; e >= 0; --e)
+        if (best[e] == most) at = best_at + e;
+    const unsigned key = order_key(most);
+    unsigned low = least < INFINITY ? ~order_key(least) : 0u;
+    const unsigned top = wave_max(key);
     // the lowest index of the largest (a thread has met its own lowest first)
-    const unsigned first = ~wave_max(most == top ? ~at : 0u);
+    const unsigned first = ~wave_max(key == top ? ~at : 0u);
+    // the smallest as the largest of the complements
     low = wave_max(low);
-    count = (int)wave_sum((u64)count);
     if (tid % WAVE == 0) s_most[wave] = top, s_at[wave] = first, s_least[wave] = low, s_count[wave] = count;
     __syncthreads();
     if (tid) return;
@@ -393,25 +439,25 @@ __global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
     reinterpret_cast<Top*>(ws + WS_TOPS)[blockIdx.x] = t;
 }
 
-// The row's largest and smallest key, the largest's lowest index, and the tokens that may be kept, from its chunks'.
-__device__ __forceinline__ Top row_top(const SampleArgs& a, const uint8_t* ws, Top* s_top) {
-    if (threadIdx.x < WAVE) {
-        Top t{0, ~0u, 0, 0};
-        for (int c = threadIdx.x; c < a.chunks; c += WAVE) {
-            const Top o = reinterpret_cast<const Top*>(ws + WS_TOPS)[c];
-            if (o.most > t.most) t.most = o.most, t.at = o.at;
-            t.least = min(t.least, o.least);
-            t.count += o.count;
-        }
-        const unsigned top = wave_max(t.most);
-        t.at = (int)~wave_max(t.most == top ? ~(unsigned)t.at : 0u);
-        t.least = ~wave_max(~t.least);
-        t.count = (int)wave_sum((u64)t.count);
-        t.most = top;
-        if (threadIdx.x == 0) *s_top = t;
+// The row's largest and smallest key, the largest's lowest index, and the tokens that may be kept, from its chunks' (by each
+// wave for itself; first: what load_top gave).
+__device__ __forceinline__ Top load_top(const SampleArgs& a, const uint8_t* ws, int c) {
+    return c < a.chunks ? reinterpret_cast<const Top*>(ws + WS_TOPS)[c] : Top{0, ~0u, 0, 0};
+}
+__device__ __forceinline__ Top row_top(const SampleArgs& a, const uint8_t* ws, Top first) {
+    Top t = first;
+    for (int c = threadIdx.x % WAVE + WAVE; c < a.chunks; c += WAVE) {
+        const Top o = load_top(a, ws, c);
+        if (o.most > t.most) t.most = o.most, t.at = o.at;
+        t.least = min(t.least, o.least);
+        t.count += o.count;
     }
-    __syncthreads();
-    return *s_top;
+    const unsigned top = wave_max(t.most);
+    t.at = (int)~wave_max(t.most == top ? ~(unsigned)t.at : 0u);
+    t.least = ~wave_max(~t.least);
+    t.count = (int)wave_sum((u64)t.count);
+    t.most = top;
+    return t;
 }
 
 // Bin of a logit: its distance to the largest, in steps that cover the tokens with a weight (40 temperatures) or, for top-k,
@@ -430,11 +476,10 @@ struct Binning {
     }
 };
 
-// adds what the workgroup's threads have to a block's sum of weights and count
+// adds what the wave's threads have to a block's sum of weights and count
 __device__ __forceinline__ void add_block(u64 sum, unsigned n, u64* mass, unsigned* count) {
-    if (!__any(n != 0)) return;
+    if (n == 0) return;
     sum = wave_sum(sum);
-    n = (unsigned)wave_sum((u64)n);
     if (threadIdx.x % WAVE == 0) atomicAdd(mass, sum), atomicAdd(count, n);
 }
 
@@ -451,47 +496,42 @@ template <int DT>
 __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     __shared__ u64 s_mass[BINS];
     __shared__ unsigned s_count[BINS];
-    __shared__ Top s_top;
+    __shared__ double s_exp[EXPS];
     const int row = blockIdx.y, tid = threadIdx.x;
-    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     uint8_t* ws = a.ws + row * a.row_bytes;
-    __shared__ double s_exp[32];
+    const Top first = load_top(a, ws, tid % WAVE);
+    Chunk<DT> chunk(a);
+    chunk.load(chunk.from);
     Rule rule = rule_of(a, row, s_exp);
-    const Top t = row_top(a, ws, &s_top);
+    for (int b = tid; b < BINS; b += ST) s_mass[b] = 0, s_count[b] = 0;
+    const Top t = row_top(a, ws, first);
     if (t.most == 0 || rule.greedy) return;
     rule.top = key_logit(t.most);
     if (rule.top_k >= t.count) rule.top_k = 0;
     const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
-    const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
+    __syncthreads();
     if (!by_count && !by_mass) {
-        for (int b = tid; b < MOST_BLOCKS; b += ST) s_mass[b] = 0, s_count[b] = 0;
-        __syncthreads();
-        for (int base = from, b = 0; base < to; base += BLOCK, ++b) {
+        chunk.each([&](const Logits<DT>& v, int, int block) __attribute__((always_inline)) {
             u64 sum = 0;
             unsigned n = 0;
-            float v[EACH];
-            load_logits<DT>(l, base + tid * EACH, a.vocab, v);
 #pragma unroll
             for (int e = 0; e < EACH; ++e) {
-                if (!order_key(v[e])) continue;
                 const double w = rule.weight(v[e]);
-                if (w >= rule.min_p) sum += fixed(w), ++n;
+                const bool keep = v[e] > -INFINITY && w >= rule.min_p;
+                sum += keep ? fixed(w) : 0;
+                n += __popcll(__ballot(keep));
             }
-            add_block(sum, n, &s_mass[b], &s_count[b]);
-        }
+            add_block(sum, n, &s_mass[block], &s_count[block]);
+        });
         __syncthreads();
         store_blocks(a, ws, s_mass, s_count);
         return;
     }
     const Binning bin(rule, t);
-    for (int b = tid; b < BINS; b += ST) s_mass[b] = 0, s_count[b] = 0;
-    __syncthreads();
-    for (int i = from + tid * EACH; i < to; i += ST * EACH) {
-        float v[EACH];
-        load_logits<DT>(l, i, a.vocab, v);
+    chunk.each([&](const Logits<DT>& v, int, int) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            if (!order_key(v[e])) continue;
+            if (!(v[e] > -INFINITY)) continue;
             const int b = bin.of(v[e]);
             if (by_count) atomicAdd(&s_count[b], 1u);
             if (by_mass) {
@@ -499,7 +539,7 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
                 if (w) atomicAdd(&s_mass[b], w);
             }
         }
-    }
+    });
     __syncthreads();
     for (int b = tid; b < BINS; b += ST) {
         if (s_count[b]) atomicAdd(reinterpret_cast<unsigned*>(ws + WS_COUNT) + b, s_count[b]);
@@ -507,35 +547,33 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     }
 }
 
-// the lowest bin with which the running sum reaches `want`; BINS if none does.  before: the sum of this thread's bins'
-// predecessors; own: its BINS / ST bins' values
-__device__ __forceinline__ void find_bin(u64 want, u64 before, const u64* own, int* s_bin) {
-    u64 sum = before;
-#pragma unroll
-    for (int e = 0; e < BINS / ST; ++e) {
-        if (sum < want && sum + own[e] >= want) *s_bin = threadIdx.x * (BINS / ST) + e;
-        sum += own[e];
-    }
-}
+constexpr int OWN = BINS / ST;           // bins of a thread
 
 template <int DT>
 __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     __shared__ u64 s_list[LIST];
     __shared__ unsigned s_listed, s_first;
-    __shared__ u64 scan[ST / WAVE];
+    __shared__ u64 scan[2 * ST / WAVE];
     __shared__ u64 s_mass[MOST_BLOCKS];
     __shared__ unsigned s_kept[MOST_BLOCKS];
-    __shared__ Top s_top;
     __shared__ int s_bin[3];
     __shared__ u64 s_at[4];
+    __shared__ double s_exp[EXPS];
     const int row = blockIdx.y, tid = threadIdx.x;
-    const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     uint8_t* ws = a.ws + row * a.row_bytes;
     RowState* state = reinterpret_cast<RowState*>(ws + WS_STATE);
-    __shared__ double s_exp[32];
+    const Top first = load_top(a, ws, tid % WAVE);
+    u64 n[OWN], m[OWN], own_n = 0, own_m = 0, all_n, all_m;
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) {
+        n[e] = reinterpret_cast<const unsigned*>(ws + WS_COUNT)[tid * OWN + e];
+        m[e] = reinterpret_cast<const u64*>(ws + WS_MASS)[tid * OWN + e];
+    }
+    Chunk<DT> chunk(a);
+    chunk.load(chunk.from);
     Rule rule = rule_of(a, row, s_exp);
     if (rule.greedy || (rule.top_k == 0 && rule.top_p >= 1.0)) return;
-    const Top t = row_top(a, ws, &s_top);
+    const Top t = row_top(a, ws, first);
     rule.top = key_logit(t.most);
     if (rule.top_k >= t.count) rule.top_k = 0;
     const bool by_count = rule.top_k != 0, by_mass = rule.top_p < 1.0;
@@ -543,67 +581,61 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     const Binning bin(rule, t);
 
     // Bins: k_bin holds the border of top-k; the sum that top-p is a part of lies between those without and with it, so the
-    // border of top-p lies in p_lo .. p_hi.
-    int k_bin = BINS, p_lo = BINS, p_hi = BINS;
-    u64 k_before = 0, mass_lo = 0, p_before = 0;      // tokens before k_bin, weights before it and before p_lo
-    u64 n[BINS / ST], m[BINS / ST], own_n = 0, own_m = 0, all_n, all_m;
+    // border of top-p lies in p_lo .. p_hi.  s_bin: these three; s_at: tokens before k_bin, weights before it, with it, and
+    // before p_lo.
 #pragma unroll
-    for (int e = 0; e < BINS / ST; ++e) {
-        n[e] = reinterpret_cast<const unsigned*>(ws + WS_COUNT)[tid * (BINS / ST) + e];
-        m[e] = reinterpret_cast<const u64*>(ws + WS_MASS)[tid * (BINS / ST) + e];
-        own_n += n[e], own_m += m[e];
-    }
-    const u64 before_n = before_and_total(own_n, scan, all_n), before_m = before_and_total(own_m, scan, all_m);
+    for (int e = 0; e < OWN; ++e) own_n += n[e], own_m += m[e];
+    u64 before_n, before_m;
     if (tid < 3) s_bin[tid] = BINS;
-    __syncthreads();
-    if (by_count) find_bin((u64)rule.top_k, before_n, n, &s_bin[0]);
-    __syncthreads();
-    k_bin = s_bin[0];
-    if (tid == 0) s_at[0] = s_at[2] = 0, s_at[1] = s_at[3] = all_m;
-    __syncthreads();
-    if (k_bin < BINS && k_bin / (BINS / ST) == tid) {
+    if (tid == 0) s_listed = 0;
+    for (int b = tid; b < MOST_BLOCKS; b += ST) s_mass[b] = 0, s_kept[b] = 0;
+    before_and_total(own_n, own_m, scan, before_n, before_m, all_n, all_m);
+    // the lowest bin with which a sum reaches `want`; f(weights and tokens before it, with it)
+    auto find_bin = [&](u64 want, bool tokens, int which, auto f) __attribute__((always_inline)) {
         u64 c = before_n, w = before_m;
-        for (int e = 0; e < k_bin % (BINS / ST); ++e) c += n[e], w += m[e];
-        s_at[0] = c, s_at[1] = w, s_at[3] = w + m[k_bin % (BINS / ST)];
+#pragma unroll
+        for (int e = 0; e < OWN; ++e) {
+            const u64 sum = tokens ? c : w, with = sum + (tokens ? n[e] : m[e]);
+            if (sum < want && with >= want) s_bin[which] = tid * OWN + e, f(c, w, w + m[e]);
+            c += n[e], w += m[e];
+        }
+    };
+    u64 k_before = 0, mass_lo = all_m, mass_hi = all_m;
+    int k_bin = BINS;
+    if (by_count) {
+        find_bin((u64)rule.top_k, true, 0, [&](u64 c, u64 w, u64 with) { s_at[0] = c, s_at[1] = w, s_at[2] = with; });
+        __syncthreads();
+        k_bin = s_bin[0];                                // (found: there are more tokens than top_k)
+        k_before = s_at[0], mass_lo = s_at[1], mass_hi = s_at[2];
     }
-    __syncthreads();
-    k_before = s_at[0], mass_lo = s_at[1];
+    int p_lo = BINS, p_hi = BINS;
+    u64 p_before = 0;
     if (by_mass) {
-        const double lo = ceil(rule.top_p * (double)mass_lo), hi = ceil(rule.top_p * (double)s_at[3]);
-        find_bin(lo > 1.0 ? (u64)lo : 1, before_m, m, &s_bin[1]);
-        find_bin(hi > 1.0 ? (u64)hi : 1, before_m, m, &s_bin[2]);
+        const double lo = ceil(rule.top_p * (double)mass_lo), hi = ceil(rule.top_p * (double)mass_hi);
+        find_bin(lo > 1.0 ? (u64)lo : 1, false, 1, [&](u64, u64 w, u64) { s_at[3] = w; });
+        find_bin(hi > 1.0 ? (u64)hi : 1, false, 2, [&](u64, u64, u64) {});
         __syncthreads();
         p_lo = s_bin[1], p_hi = s_bin[2];
-        if (p_lo < BINS && p_lo / (BINS / ST) == tid) {
-            u64 w = before_m;
-            for (int e = 0; e < p_lo % (BINS / ST); ++e) w += m[e];
-            s_at[2] = w;
-        }
-        __syncthreads();
-        p_before = s_at[2];
+        p_before = p_lo < BINS ? s_at[3] : 0;
     }
     if (blockIdx.x == 0 && tid == 0) state->mass_lo = mass_lo, state->p_before = p_before, state->k_bin = k_bin, state->k_before = (int)k_before;
     const int border = by_mass ? p_lo : k_bin;           // bins before it are kept for certain
 
-    for (int b = tid; b < MOST_BLOCKS; b += ST) s_mass[b] = 0, s_kept[b] = 0;
-    if (tid == 0) s_listed = 0;
-    __syncthreads();
-    const int from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.vocab);
-    for (int base = from, block = 0; base < to; base += BLOCK, ++block) {
+    chunk.each([&](const Logits<DT>& v, int i, int block) __attribute__((always_inline)) {
         u64 sum = 0;
-        unsigned n = 0, in_list = 0;               // (a bit for each)
-        float v[EACH];
-        load_logits<DT>(l, base + tid * EACH, a.vocab, v);
+        unsigned kept = 0, in_list = 0;            // (a bit for each)
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            if (!order_key(v[e])) continue;
+            const bool may = v[e] > -INFINITY;
             const int b = bin.of(v[e]);
-            if (b < border) {
+            bool keep = may && b < border;
+            if (__any(keep)) {
                 const double w = rule.weight(v[e]);
-                if (w >= rule.min_p) sum += fixed(w), ++n;
-            } else if (b == k_bin || (by_mass && b <= p_hi)) {
-                in_list |= 1u << e;
+                keep = keep && w >= rule.min_p;
+                sum += keep ? fixed(w) : 0;
+                kept += __popcll(__ballot(keep));
             }
+            if (may && b >= border && (b == k_bin || (by_mass && b <= p_hi))) in_list |= 1u << e;
         }
         if (__any(in_list != 0)) {
             const int mine = __popc(in_list), incl = wave_incl_scan(mine);
@@ -613,12 +645,12 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
 #pragma unroll
             for (int e = 0; e < EACH; ++e) {
                 if (!(in_list >> e & 1)) continue;
-                if (at < LIST) s_list[at] = (u64)order_key(v[e]) << 32 | ~(unsigned)(base + tid * EACH + e);
+                if (at < LIST) s_list[at] = (u64)order_key(v[e]) << 32 | ~(unsigned)(i + e);
                 ++at;
             }
         }
-        add_block(sum, n, &s_mass[block], &s_kept[block]);
-    }
+        add_block(sum, kept, &s_mass[block], &s_kept[block]);
+    });
     __syncthreads();
     store_blocks(a, ws, s_mass, s_kept);
     // one addition to the row's count for all of the workgroup's tokens: each waits for the one before (with one for every
@@ -632,20 +664,26 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
 // The token of a row: a workgroup each.
 template <int DT>
 __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
-    __shared__ u64 s_list[LIST];
-    __shared__ u64 scan[ST / WAVE];
+    __shared__ __align__(16) u64 s_list[LIST];
+    __shared__ u64 scan[2 * ST / WAVE];
     __shared__ u64 s_mass[MOST_BLOCKS];
     __shared__ unsigned s_kept[MOST_BLOCKS];
-    __shared__ Top s_top;
     __shared__ u64 s_sum;
     __shared__ unsigned s_n;
+    __shared__ double s_exp[EXPS];
     const int row = blockIdx.x, tid = threadIdx.x;
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     const uint8_t* ws = a.ws + row * a.row_bytes;
+    const Top first = load_top(a, ws, tid % WAVE);
     const RowState state = *reinterpret_cast<const RowState*>(ws + WS_STATE);
-    __shared__ double s_exp[32];
+    // (whatever there is of it)
+    const u64 in_list = reinterpret_cast<const u64*>(ws + WS_LIST)[tid];
+    if (tid < a.blocks) {
+        s_mass[tid] = reinterpret_cast<const u64*>(ws + WS_BLOCK_MASS)[tid];
+        s_kept[tid] = reinterpret_cast<const unsigned*>(ws + WS_BLOCK_KEPT)[tid];
+    }
     Rule rule = rule_of(a, row, s_exp);
-    const Top t = row_top(a, ws, &s_top);
+    const Top t = row_top(a, ws, first);
     if (t.most == 0 || rule.greedy) {
         if (tid == 0) {
             a.token[row] = t.most ? t.at : -1;
@@ -662,24 +700,25 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     const u64 k_before = (u64)state.k_before, mass_lo = state.mass_lo, p_before = state.p_before;
     const unsigned listed = by_count || by_mass ? state.listed : 0;
     if (listed > LIST) {
+        __syncthreads();
         whole_row<DT>(a, row, rule, s_list, scan);
         return;
-    }
-    for (int b = tid; b < a.blocks; b += ST) {
-        s_mass[b] = reinterpret_cast<const u64*>(ws + WS_BLOCK_MASS)[b];
-        s_kept[b] = reinterpret_cast<const unsigned*>(ws + WS_BLOCK_KEPT)[b];
     }
     // the list, largest first: short ones by counting the larger ones of each, long ones by a bitonic network
     int size = WAVE;
     while (size < (int)listed) size *= 2;
     for (int i = tid; i < size; i += ST)
-        s_list[i] = i < (int)listed ? reinterpret_cast<const u64*>(ws + WS_LIST)[i] : 0ull;
+        s_list[i] = i >= (int)listed ? 0ull : i < ST ? in_list : reinterpret_cast<const u64*>(ws + WS_LIST)[i];
     __syncthreads();
     if (listed <= ST) {
         const u64 mine = tid < (int)listed ? s_list[tid] : 0;
         int rank = 0;
-#pragma unroll 8
-        for (int i = 0; i < (int)listed; ++i) rank += s_list[i] > mine;
+        // (past the list are zeros)
+#pragma unroll 4
+        for (int i = 0; i < (int)listed; i += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&s_list[i]);
+            rank += (o.x > mine) + (o.y > mine);
+        }
         __syncthreads();
         if (tid < (int)listed) s_list[rank] = mine;
         __syncthreads();
@@ -726,8 +765,9 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
                 own += w[e];
                 if (i >= begin_k) own_k += w[e];
             }
-            before_and_total(own_k, scan, in_k);
-            const u64 before = p_before + before_and_total(own, scan, all);
+            u64 before, before_k;
+            before_and_total(own, own_k, scan, before, before_k, all, in_k);
+            before += p_before;
             const double p = ceil(rule.top_p * (double)(mass_lo + in_k));
             const u64 want = p > 1.0 ? (u64)p : 1;
             // (past p_hi there are tokens that the list leaves out, but the sum has reached `want` before)
@@ -756,10 +796,9 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     }
 
     // the block that the random number falls into
-    u64 total, kept;
+    u64 total, kept, before, kept_before;
     const u64 mine = tid < a.blocks ? s_mass[tid] : 0;
-    const u64 before = before_and_total(mine, scan, total);
-    before_and_total(tid < a.blocks ? (u64)s_kept[tid] : 0ull, scan, kept);
+    before_and_total(mine, tid < a.blocks ? (u64)s_kept[tid] : 0ull, scan, before, kept_before, total, kept);
     const float u = a.u[row];
     u64 target = u > 0.0f ? (u64)((double)u * (double)total) : 0;
     if (u >= 1.0f || target >= total) target = total - 1;
@@ -768,8 +807,8 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     __syncthreads();
     // and the token in it: every thread has a run of eight
     const int from = (int)s_n * BLOCK + tid * EACH;
-    float v[EACH];
-    load_logits<DT>(l, from, a.vocab, v);
+    Logits<DT> v;
+    v.load(l, from, a.vocab);
     u64 w[EACH], sum = 0, in_block;
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
