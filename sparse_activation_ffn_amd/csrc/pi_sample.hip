@@ -323,8 +323,9 @@ __device__ void whole_row(const SampleArgs& a, int row, const Rule& rule, u64* m
 //                    has either rule)                                                                        17.8  13.2   5.8
 //   k_sample_pick    a workgroup to each row: sorts the list, finds the border and the token                 12.7   9.8   7.3
 // The whole call: 55.3, 36.4 and 21.5 us.  A dependent launch costs some 4 us here; what is left are the chains of sums in
-// each and weights in 64 bits (6 of k_sample_count's 17.5), neither bytes nor atomics.  (A row's last workgroup doing the pick in the launch before
-// needs fences between the dies, which write back and drop whole caches: 26 us in place of 13 for one row, 108 for 64.)
+// each and weights in 64 bits (6 of k_sample_count's 17.5), neither bytes nor atomics.  (A row's last workgroup doing the pick
+// in the launch before needs fences between the dies, which write back and drop whole caches: 26 us in place of 13 for one
+// row, 108 for 64.)  Short rows take one launch, k_sample_row.
 // Sums are integers, so that neither their order nor that of the list matters.  A row whose border bins hold more than
 // LIST tokens (equal logits, or a border far below the others) is done by k_sample_pick alone, from the start: 0.5 to
 // 0.9 ms for 128000 logits, equal ones or normal ones of a tenth of the temperature beside one of -1e30.
@@ -384,8 +385,8 @@ struct Chunk {
     }
 };
 
-template <int DT>
-__global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
+template <int DT, bool ALONE>
+__device__ __forceinline__ void top_stage(const SampleArgs& a) {
     __shared__ unsigned s_most[ST / WAVE], s_least[ST / WAVE], s_at[ST / WAVE];
     __shared__ int s_count[ST / WAVE];
     const int row = blockIdx.y, tid = threadIdx.x, wave = tid / WAVE;
@@ -393,9 +394,11 @@ __global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) {
     chunk.load(chunk.from);
     uint8_t* ws = a.ws + row * a.row_bytes;
     // what the later launches add to
-    for (int b = blockIdx.x * ST + tid; b < BINS; b += gridDim.x * ST) {
-        reinterpret_cast<u64*>(ws + WS_MASS)[b] = 0;
-        reinterpret_cast<unsigned*>(ws + WS_COUNT)[b] = 0;
+    if constexpr (!ALONE) {
+        for (int b = blockIdx.x * ST + tid; b < BINS; b += gridDim.x * ST) {
+            reinterpret_cast<u64*>(ws + WS_MASS)[b] = 0;
+            reinterpret_cast<unsigned*>(ws + WS_COUNT)[b] = 0;
+        }
     }
     if (blockIdx.x == 0 && tid == 0) reinterpret_cast<RowState*>(ws + WS_STATE)->listed = 0;
 
@@ -492,8 +495,8 @@ __device__ __forceinline__ void store_blocks(const SampleArgs& a, uint8_t* ws, c
     }
 }
 
-template <int DT>
-__global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
+template <int DT, bool ALONE>
+__device__ __forceinline__ void count_stage(const SampleArgs& a) {
     __shared__ u64 s_mass[BINS];
     __shared__ unsigned s_count[BINS];
     __shared__ double s_exp[EXPS];
@@ -542,15 +545,20 @@ __global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) {
     });
     __syncthreads();
     for (int b = tid; b < BINS; b += ST) {
-        if (s_count[b]) atomicAdd(reinterpret_cast<unsigned*>(ws + WS_COUNT) + b, s_count[b]);
-        if (s_mass[b]) atomicAdd(reinterpret_cast<u64*>(ws + WS_MASS) + b, s_mass[b]);
+        if constexpr (ALONE) {
+            reinterpret_cast<unsigned*>(ws + WS_COUNT)[b] = s_count[b];
+            reinterpret_cast<u64*>(ws + WS_MASS)[b] = s_mass[b];
+        } else {
+            if (s_count[b]) atomicAdd(reinterpret_cast<unsigned*>(ws + WS_COUNT) + b, s_count[b]);
+            if (s_mass[b]) atomicAdd(reinterpret_cast<u64*>(ws + WS_MASS) + b, s_mass[b]);
+        }
     }
 }
 
 constexpr int OWN = BINS / ST;           // bins of a thread
 
-template <int DT>
-__global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
+template <int DT, bool ALONE>
+__device__ __forceinline__ void list_stage(const SampleArgs& a) {
     __shared__ u64 s_list[LIST];
     __shared__ unsigned s_listed, s_first;
     __shared__ u64 scan[2 * ST / WAVE];
@@ -656,14 +664,19 @@ __global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) {
     // one addition to the row's count for all of the workgroup's tokens: each waits for the one before (with one for every
     // wave and step 48 rows of 50007 took 16 us here)
     if (s_listed == 0) return;
-    if (tid == 0) s_first = atomicAdd(&state->listed, s_listed);
+    if (tid == 0) {
+        if constexpr (ALONE)
+            s_first = 0, state->listed = s_listed;
+        else
+            s_first = atomicAdd(&state->listed, s_listed);
+    }
     __syncthreads();
     for (unsigned i = tid; i < s_listed && s_first + i < LIST; i += ST) reinterpret_cast<u64*>(ws + WS_LIST)[s_first + i] = s_list[i];
 }
 
 // The token of a row: a workgroup each.
 template <int DT>
-__global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
+__device__ __forceinline__ void pick_stage(const SampleArgs& a, int row) {
     __shared__ __align__(16) u64 s_list[LIST];
     __shared__ u64 scan[2 * ST / WAVE];
     __shared__ u64 s_mass[MOST_BLOCKS];
@@ -671,7 +684,7 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     __shared__ u64 s_sum;
     __shared__ unsigned s_n;
     __shared__ double s_exp[EXPS];
-    const int row = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x;
     const uint8_t* l = a.logits + row * a.stride * (DT == F16 ? 2 : 4);
     const uint8_t* ws = a.ws + row * a.row_bytes;
     const Top first = load_top(a, ws, tid % WAVE);
@@ -832,11 +845,38 @@ __global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) {
     }
 }
 
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_top(SampleArgs a) { top_stage<DT, false>(a); }
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_count(SampleArgs a) { count_stage<DT, false>(a); }
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_list(SampleArgs a) { list_stage<DT, false>(a); }
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_pick(SampleArgs a) { pick_stage<DT>(a, blockIdx.x); }
+
+// All of it for a row of one chunk, by one workgroup: what the stages leave for each other has one writer.
+template <int DT>
+__global__ __launch_bounds__(ST) void k_sample_row(SampleArgs a) {
+    top_stage<DT, true>(a);
+    __syncthreads();
+    count_stage<DT, true>(a);
+    __syncthreads();
+    if (a.top_k || a.top_p) list_stage<DT, true>(a);
+    __syncthreads();
+    pick_stage<DT>(a, blockIdx.y);
+}
+
 size_t sample_bytes(int rows, int) { return (size_t)rows * WS_ROW; }
+
+// Short rows go by one workgroup each, as long as each has a unit of its own (its LDS leaves room for one): launches saved
+// against chunks side by side.  us with top-k and with top-p, float32, one launch and four:
+//   1 x 1000  15.7 17.2, 19.6 21.3    1 x 8192    15.9 20.8, 18.2 21.3     1 x 16384    19.3 27.1, 18.1 21.3
+//   64 x 8192 17.4 21.7, 21.3 24.8    256 x 8192  18.3 23.1, 28.2 33.9     1000 x 8192  68.3 86.7, 52.9 69.1
+bool row_alone(const SampleArgs& a) { return a.vocab <= 8192 && a.rows <= 256; }
 
 // Chunks of a row so that some 512 workgroups have work, of 4096 logits at least.
 void chunks_of(SampleArgs& a) {
-    const int want = std::max(1, 512 / a.rows);
+    const int want = row_alone(a) ? 1 : std::max(1, 512 / a.rows);
     a.chunk = std::max(1, (int)(((int64_t)a.vocab + (int64_t)want * BLOCK - 1) / ((int64_t)want * BLOCK))) * BLOCK;
     a.chunks = (a.vocab + a.chunk - 1) / a.chunk;
     a.blocks = (a.vocab + BLOCK - 1) / BLOCK;
@@ -845,6 +885,7 @@ void chunks_of(SampleArgs& a) {
 template <int DT>
 pi_status sample(const SampleArgs& a, hipStream_t s) {
     const dim3 grid(a.chunks, a.rows), block(ST);
+    if (row_alone(a)) return launch(PI_K_SAMPLE, k_sample_row<DT>, grid, block, 0, s, a);
     TRY(launch(PI_K_SAMPLE, k_sample_top<DT>, grid, block, 0, s, a));
     TRY(launch(PI_K_SAMPLE, k_sample_count<DT>, grid, block, 0, s, a));
     if (a.top_k || a.top_p) TRY(launch(PI_K_SAMPLE, k_sample_list<DT>, grid, block, 0, s, a));

@@ -222,3 +222,25 @@ def test_wrong_tensors():
             pb.pi_sample(a["logits"], a["rule"], a["u"], a["token"], ws=ws)
     with pytest.raises(pb.PiError):
         pb.pi_sample(l, pb.make_sample_rule(), u, tok, ws=ws[:0])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("vocab", [1, 1000, 4096, 4097, 8191, 8192])
+def test_short_rows_and_long_rows_agree(vocab, dtype):
+    """A row alone, among 300, and with tokens that are never kept behind it: the same bits.  Equal logits are among them."""
+    rng = np.random.default_rng([vocab, 5])
+    rows = 300
+    l = rows_of(rng, rows, vocab, dtype)
+    l[::7] = np.round(l[::7])
+    l[::50], l[3::50, ::2] = 1.0, -np.inf
+    u = rng.random(rows).astype(np.float32)
+    t = np.where(np.arange(rows) % 5, rng.uniform(0.3, 2, rows), 0).astype(np.float32)
+    k, p = rng.integers(-5, 300, rows).astype(np.int32), rng.uniform(0.2, 1.2, rows).astype(np.float32)
+    padded = np.concatenate([l, np.full((rows, 8300 - vocab), -np.inf, l.dtype)], 1)
+    for rules in (dict(t=t), dict(t=t, k=k), dict(t=t, p=p), dict(t=t, k=k, p=p, m=0.1 * p)):
+        many = run(l, u, **rules)
+        for lo, hi in ((0, 100), (100, 101), (101, 300)):
+            few = run(l[lo:hi], u[lo:hi], **{name: v[lo:hi] for name, v in rules.items()})
+            assert all(np.array_equal(a, b[lo:hi]) for a, b in zip(few, many)), (lo, hi)
+        assert all(np.array_equal(a, b) for a, b in zip(run(padded, u, **rules), many))
+        assert all(np.array_equal(a, b[:200]) for a, b in zip(run(padded[:200], u[:200], **{n: v[:200] for n, v in rules.items()}), many))
