@@ -202,7 +202,9 @@ __device__ __forceinline__ void store_out4(const ProductArgs& p, int i, int j, f
 // instruction, no LDS and no barrier on the way.  A workgroup takes NT x 16 rows of w and 16 of a; its NW waves share out K in
 // pieces of 512 elements and join their sums in LDS in a fixed order.  A piece is what is loaded at once, so that both
 // halves of a 128-byte line are asked for together and a row's scales in one load: in pieces of 128 the lines had left the
-// 32 KB of the first-level cache before their other half was asked for (1 x 10240 x 8192: 18.4 us).
+// 32 KB of the first-level cache before their other half was asked for (1 x 10240 x 8192: 18.4 us, 14.5 so).  A load
+// of 16 rows takes the path to memory some 64 cycles whatever it brings, which is why tiles through LDS are faster where
+// there are enough of them; 1 x 4096 x 8192 takes 6.5 us with the launch.
 template <int MODE, int MT, int NT, int STEPS>
 struct Piece {
     Frag<false> w[STEPS][NT];
@@ -317,9 +319,12 @@ pi_status launch_few(const ProductArgs& p, hipStream_t s) {
 
 // ---- many rows of a ----------------------------------------------------------------
 //
-// Tiles of BM rows of a by BN rows of w through LDS: while a stage of KS elements is multiplied, the next one comes in by
-// direct loads into the other buffer.  A row's 16-byte pieces are permuted by the row, so that the 16 rows that a fragment read
-// takes at one piece lie in 16 different pieces of 256 bytes.  Scales come 512 elements at a time, through registers.
+// Tiles of BM rows of a by BN rows of w through LDS, in a ring of stages of KS elements: while one is multiplied, the RING - 1
+// after it come in by direct loads, which are waited for by count.  A row's 16-byte pieces are permuted by the row, so that the
+// 16 rows that a fragment read takes at one piece lie in 16 different pieces of 256 bytes.  Scales come 512 elements at a time,
+// by direct loads where K is a multiple of 512, else through registers.  The matrix cores bound large products, bytes and the
+// depth of the ring small ones.  us (TFLOP/s), 4096 x 10240 x 8192: MXFP8 to f16 278 (2470), to float32 513 (1340: half the
+// rate, and both sides turned to bfloat16 by every wave that reads them), MXFP4 235 (2930).
 __device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
@@ -618,9 +623,13 @@ pi_status launch_many(const ProductArgs& p, hipStream_t s) {
 }
 
 // Which form a product takes.  The chip holds one or two workgroups per unit; forms whose tiles are fewer split K so that
-// each of the 256 units has one, in pieces of 1024 elements at least, and join (a launch of 3 us).  us, MXFP8 to f16, one
-// and several splits:   32 x 7168 x 8192  16.3, two 14.4    48 x 7168 x 8192  24.8, four 17.0
-//                       64 x 10240 x 8192 23.5, three 22.2   128 x 10240 x 8192 60, three 35.5
+// each of the 256 units has one, in pieces of 1024 elements at least, and join (a launch of 4 us).  us, MXFP8 to f16, by
+// splits (* what the rule takes):
+//                       1      2      3      4      6
+//   32 x 7168 x 8192    18.4   14.0*  15.4   15.0   17.3
+//   48 x 7168 x 8192    28.4   19.9   17.4   15.3*  21.7
+//   64 x 10240 x 8192   29.7   21.8   20.1*  26.3   26.5
+//   128 x 10240 x 8192  50.9   34.7   30.3*  33.3   33.4
 enum Form { WAVES_SHARE_K, TILE_16, TILE_32, TILE_64, TILE_128, TILE_WIDE };
 struct ProductPlan {
     Form form;
@@ -629,14 +638,14 @@ struct ProductPlan {
 
 ProductPlan plan_product(int64_t m, int64_t n, int64_t k) {
     const Form form = m <= 16 ? TILE_16 : m <= 32 ? TILE_32 : m <= 64 ? TILE_64 : TILE_128;
-    const int64_t rows = form == TILE_128 ? 128 : 64 , cols = form <= TILE_32 ? 64 : 128;
+    const int64_t rows = form == TILE_128 ? 128 : 64, cols = form <= TILE_32 ? 64 : 128;
     const int64_t tiles = (m + rows - 1) / rows * ((n + cols - 1) / cols);
-    // Tiles of 128 x 256 take two thirds of the time of two of 128 x 128, where there are enough (4096 x 10240 x 8192: 327
-    // us and 400; 1024 x 8192 x 8192, 256 of them: 91 and 79).
+    // Tiles of 128 x 256 take four fifths of the time of two of 128 x 128, where there are enough (4096 x 10240 x 8192: 282
+    // us and 358; 1024 x 8192 x 8192, 256 of them: 80 and 77; 512 x 8192 x 8192, 128 of them: 78 and 53).
     if (form == TILE_128 && (m + 127) / 128 * ((n + 255) / 256) > 256) return {TILE_WIDE, 1};
     const int64_t splits = std::max<int64_t>(1, std::min(256 / tiles, k / (2 * LONG)));
-    // Sixteen rows or fewer: one wave per 16 rows of w and eighth of K where tiles are too few, without a join (1 x 1024 x
-    // 8192: 5.3 us; 1 x 10240 x 8192: 14.4, tiles of 64 rows of w 12.8).
+    // Sixteen rows or fewer: one wave per 16 rows of w and eighth of K where tiles of 64 rows of w are too few, without a
+    // join (us, and tiles: 1 x 1024 x 8192 5.4, 10.6; 1 x 4096 6.5, 10.5; 1 x 8192 11.7, 11.8; 1 x 10240 14.5, 12.4).
     if (form == TILE_16) return {tiles < 128 ? WAVES_SHARE_K : TILE_16, 1};
     return {form, (int)splits};
 }

@@ -38,7 +38,8 @@ struct NormArgs {
 // element: the HBM rate bounds it, a launch and two dependent latencies where there are few rows.  So a row stays in
 // registers between the sum of its squares and its outputs: 8 elements (a 16-byte load of f16) per thread and chunk, a
 // row on 8 to 64 lanes of a wave (heads) or on a workgroup.  The squares are summed in 64 bits: exact products of
-// f16, and no overflow for float32.
+// f16, and no overflow for float32.  us: 4099 tokens of 64 heads of 128 in f16, 27.9 (4.8 TB/s); 8191 rows of 8192 in f16
+// with an f16 delta, to their sum and MXFP8, 91 (5.2 TB/s); one row of 7168 with a float32 delta, 3.4.
 
 template <int CTRL>
 __device__ __forceinline__ double add_dpp(double v) {
@@ -288,7 +289,9 @@ __global__ __launch_bounds__(NT) void k_rms_norm_any(NormArgs a) {
 // ---- microscaled quantisation ----------------------------------------------------------
 //
 // Bytes alone bound both directions.  A thread takes 8 elements, a quad of lanes a block; 2^log lanes a row, so that
-// short rows fill a wave.
+// short rows fill a wave.  One piece of a row to a thread, in as many workgroups as that takes: two, four and eight rows of a
+// thread in flight at once took 1, 5 and 9 us longer (10240 x 8192 f16 to MXFP4: 39.7 us, 5.3 TB/s, back 43.2; on other
+// data every time, one after the other, both take 97, 4.4 TB/s, with one row or four).
 struct ConvertArgs {
     const uint8_t* x;
     uint8_t* out;
@@ -298,78 +301,59 @@ struct ConvertArgs {
     int rows, cols, log;
 };
 
-template <int XT, int FMT, bool VEC, int ROWS>
+template <int XT, int FMT, bool VEC>
 __global__ __launch_bounds__(NT) void k_mx_quantize(ConvertArgs a) {
     constexpr int ES = XT == F16 ? 2 : 4;
     const int at = ((int)blockIdx.y << a.log | (int)(threadIdx.x & ((1u << a.log) - 1))) * 8;
     if (at >= a.cols) return;
-    const int per = NT >> a.log, step = gridDim.x * per;
-    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += step * ROWS) {
-        float v[ROWS][8];
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            if (row + i * step < a.rows) load8<XT, VEC>(a.x + (int64_t)(row + i * step) * a.stride + (int64_t)at * ES, v[i]);
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            if (row + i * step < a.rows) store_block<FMT>(v[i], (int64_t)(row + i * step) * a.cols + at, a.codes, a.scales);
+    const int per = NT >> a.log;
+    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += gridDim.x * per) {
+        float v[8];
+        load8<XT, VEC>(a.x + (int64_t)row * a.stride + (int64_t)at * ES, v);
+        store_block<FMT>(v, (int64_t)row * a.cols + at, a.codes, a.scales);
     }
 }
 
-template <int XT, int FMT, bool VEC, int ROWS>
+template <int XT, int FMT, bool VEC>
 __global__ __launch_bounds__(NT) void k_mx_dequantize(ConvertArgs a) {
     constexpr int ES = XT == F16 ? 2 : 4;
     const int at = ((int)blockIdx.y << a.log | (int)(threadIdx.x & ((1u << a.log) - 1))) * 8;
     if (at >= a.cols) return;
-    const int per = NT >> a.log, step = gridDim.x * per;
-    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += step * ROWS) {
-        u2 c[ROWS];
-        int scale[ROWS];
+    const int per = NT >> a.log;
+    for (int row = blockIdx.x * per + (threadIdx.x >> a.log); row < a.rows; row += gridDim.x * per) {
+        const int64_t in_all = (int64_t)row * a.cols + at;
+        u2 c;
+        if constexpr (FMT == PI_MXFP8)
+            c = *reinterpret_cast<const u2*>(a.codes + in_all);
+        else
+            c.x = *reinterpret_cast<const unsigned*>(a.codes + in_all / 2);
+        const int scale = a.scales[in_all / 32];
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            if (row + i * step >= a.rows) continue;
-            const int64_t in_all = (int64_t)(row + i * step) * a.cols + at;
-            if constexpr (FMT == PI_MXFP8)
-                c[i] = *reinterpret_cast<const u2*>(a.codes + in_all);
-            else
-                c[i].x = *reinterpret_cast<const unsigned*>(a.codes + in_all / 2);
-            scale[i] = a.scales[in_all / 32];
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            if (row + i * step >= a.rows) continue;
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (FMT == PI_MXFP8) {
-                    const auto p = e % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][e / 2], true)
-                                         : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][e / 2], false);
-                    v[2 * e] = p[0], v[2 * e + 1] = p[1];
-                } else {
-                    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i].x >> (8 * e), 1.0f, 0);
-                    v[2 * e] = p[0], v[2 * e + 1] = p[1];
-                }
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (FMT == PI_MXFP8) {
+                const auto p = e % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[e / 2], true)
+                                     : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[e / 2], false);
+                v[2 * e] = p[0], v[2 * e + 1] = p[1];
+            } else {
+                const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.x >> (8 * e), 1.0f, 0);
+                v[2 * e] = p[0], v[2 * e + 1] = p[1];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = scale[i] == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[e], scale[i] - 127);
-            store8<XT, VEC>(a.out + (int64_t)(row + i * step) * a.stride + (int64_t)at * ES, v);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = scale == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[e], scale - 127);
+        store8<XT, VEC>(a.out + (int64_t)row * a.stride + (int64_t)at * ES, v);
     }
 }
 
-// Several rows of a thread are in flight at once where there are enough for it: 8192 workgroups otherwise.
-template <bool QUANTIZE, int XT, int FMT, bool VEC, int ROWS>
-pi_status launch_rows(const ConvertArgs& a, hipStream_t s) {
-    const int per = (NT >> a.log) * ROWS;
-    const dim3 grid(std::min((a.rows + per - 1) / per, 1 << 16), ((a.cols / 8) + (1 << a.log) - 1) >> a.log);
-    if constexpr (QUANTIZE)
-        return launch(PI_K_MX_CONVERT, k_mx_quantize<XT, FMT, VEC, ROWS>, grid, dim3(NT), 0, s, a);
-    else
-        return launch(PI_K_MX_CONVERT, k_mx_dequantize<XT, FMT, VEC, ROWS>, grid, dim3(NT), 0, s, a);
-}
 template <bool QUANTIZE, int XT, int FMT, bool VEC>
 pi_status launch_convert(const ConvertArgs& a, hipStream_t s) {
-    const bool many = (int64_t)a.rows * a.cols >= (int64_t)8192 * NT * 8;
-    return many ? launch_rows<QUANTIZE, XT, FMT, VEC, 4>(a, s) : launch_rows<QUANTIZE, XT, FMT, VEC, 1>(a, s);
+    const int per = NT >> a.log;
+    const dim3 grid(std::min((a.rows + per - 1) / per, 1 << 16), ((a.cols / 8) + (1 << a.log) - 1) >> a.log);
+    if constexpr (QUANTIZE)
+        return launch(PI_K_MX_CONVERT, k_mx_quantize<XT, FMT, VEC>, grid, dim3(NT), 0, s, a);
+    else
+        return launch(PI_K_MX_CONVERT, k_mx_dequantize<XT, FMT, VEC>, grid, dim3(NT), 0, s, a);
 }
 
 template <bool QUANTIZE>
@@ -413,6 +397,9 @@ pi_status launch_norm(const NormArgs& a, hipStream_t s) {
     return launch(PI_K_NORM, k_rms_norm<XT, TPR, C, NONE>, grid, block, 0, s, a);
 }
 
+// Threads of a row: one chunk each up to 8192 elements.  8192 elements on 1024 threads, and four chunks each on 256, us of
+// f16 with an f16 delta, a sum, and MXFP8 or y: 1024 rows 14.4 and 14.0, 15.6 and 13.2; 8191 rows 95.6 and 94.8, 90.6 and
+// 102.5; one row's kernel 4.2, 6.3.
 template <int XT>
 pi_status norm_by_size(const NormArgs& a, bool vec, hipStream_t s) {
     if (!vec || a.d > 8 * 2048) return launch(PI_K_NORM, k_rms_norm_any<XT>, dim3(a.rows), dim3(NT), 0, s, a);
