@@ -98,7 +98,7 @@ struct Rule {
     double inv_t, min_p, top_p;          // min_p 0 and top_p 1: none
     float top;                           // the largest logit
     int top_k;                           // 0: none
-    bool greedy;
+    bool greedy;                         // the first token alone is kept
 
     const double* table;                 // of exp_by
 
@@ -120,12 +120,12 @@ __device__ __forceinline__ Rule rule_of(const SampleArgs& a, int row, double* ta
     fill_exps(table);
     r.table = table;
     const float t = a.temperature ? a.temperature[row] : 1.0f;
-    r.greedy = !(t > 0.0f);
+    const float p = a.top_p ? a.top_p[row] : 1.0f, m = a.min_p ? a.min_p[row] : 0.0f;
+    r.greedy = !(t > 0.0f) || m > 1.0f;  // (no weight reaches a min-p above 1)
     r.inv_t = r.greedy ? 1.0 : 1.0 / (double)t;
     r.top_k = a.top_k ? max(a.top_k[row], 0) : 0;
-    const float p = a.top_p ? a.top_p[row] : 1.0f, m = a.min_p ? a.min_p[row] : 0.0f;
     r.top_p = p < 1.0f ? (double)p : 1.0;
-    r.min_p = m > 0.0f ? fmin((double)m, 1.0) : 0.0;
+    r.min_p = m > 0.0f ? (double)m : 0.0;
     return r;
 }
 
