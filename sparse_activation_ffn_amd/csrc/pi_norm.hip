@@ -109,11 +109,13 @@ struct Scale {
         } else {
             const double v = (double)s * r * (double)w;
             y = (float)v;
-            rest = ODD ? (float)(v - (double)y) : 0.0f;
+            // (its sign alone: next to a subnormal y the difference is below float32's smallest number)
+            const double more = ODD ? v - (double)y : 0.0;
+            rest = more < 0.0 ? -1.0f : more > 0.0 ? 1.0f : 0.0f;
         }
         if (ODD && fabsf(y) < INFINITY && rest != 0.0f) {
             unsigned b = __builtin_bit_cast(unsigned, y);
-            if ((rest < 0.0f) == (y > 0.0f)) --b;
+            if ((rest < 0.0f) != (b >> 31 != 0)) --b;      // (towards 0; a y of 0 has the sign of the rest)
             y = __builtin_bit_cast(float, b | 1u);
         }
         return y;
@@ -216,16 +218,20 @@ __global__ __launch_bounds__(std::max(NT, TPR)) void k_rms_norm(NormArgs a) {
         }
         if (C > 1) load_weight(at, w);
         float v[8];
+        bool tie = false;
         if (exact) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = scale.of<true, false>(s[c].get(e), w[e]);
         } else {
+            // (the last bit of a subnormal is 2^-149 wherever it lies, so that fewer zeros end a tie's; f16 times f16 has none)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = scale.of<false, false>(s[c].get(e), w[e]);
+            for (int e = 0; e < 8; ++e) {
+                v[e] = scale.of<false, false>(s[c].get(e), w[e]);
+                tie |= fabsf(v[e]) < 0x1p-126f;
+            }
         }
         if (a.y) store8<XT, true>(y + (int64_t)at * ES, v);
         if constexpr (FORMAT != NONE) {
-            bool tie = false;
 #pragma unroll
             for (int e = 0; e < 8; ++e) tie |= may_be_tie(v[e]);
             if (__any(tie)) {

@@ -4,6 +4,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import step_ref as R  # noqa: E402
+from sparse_activation_ffn_amd import binding as pb  # noqa: E402
+from test_gpu_norm_mx import FMT, dev, host, strided  # noqa: E402
 from test_gpu_sample import run as draw  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -36,3 +39,22 @@ def test_min_p_above_one_keeps_the_first_alone(vocab, dtype):
     _, prob, kept = draw(l, u, m=np.ones(6, np.float32))
     assert list(kept) == [*many[:5], 0]
     assert np.array_equal(prob[:5], (1 / many[:5]).astype(np.float32))
+
+# ---- norm ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("form", ["fp8", "fp4"])
+@pytest.mark.parametrize("d", [256, 4096])
+@pytest.mark.parametrize("off", [0, 1])
+def test_norm_of_tiny_weights_is_rounded_once(off, d, form):
+    """y below float32's normal numbers, whose float32 lies half between two codes far more often: every code is that of y
+    itself, in rows of any alignment.  (y in 64 bits is off by 2^-50, and no y comes so near to a tie.)"""
+    rng = np.random.default_rng([d, len(form)])
+    x = rng.standard_normal((1 << 20) // d * d).reshape(-1, d).astype(np.float32)
+    w = (rng.uniform(1, 2, d) * 2.0 ** -rng.integers(125, 140, d // 32).repeat(32)).astype(np.float32)
+    mx = pb.empty_mx(len(x), d, FMT[form])
+    pb.pi_rms_norm(pb.make_norm(dev(w)), strided(x, 0, 0.0, off)[0], mx=mx)
+    torch.cuda.synchronize()
+    y = R.norm(x, w, 1e-5)
+    codes, want = host(mx._keep[0]), R.packed(R.codes(y, form), form)
+    assert np.array_equal(host(mx._keep[1]), R.scales(y, form))
+    assert int((codes != want).sum()) == 0
