@@ -419,6 +419,18 @@ pi_status norm_by_size(const NormArgs& a, bool vec, hipStream_t s) {
     return launch_norm<XT, 1024, 2>(a, s);
 }
 
+// Whether rows at i * s1 + j * s2 (i < n1, j < n2; s1, s2 >= len) share memory, each `len` long.  Two rows' places differ by
+// k * s1 + l * s2; for every k the one l that can bring that inside a row is looked at.
+bool rows_collide(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len) {
+    if (n1 > n2) std::swap(n1, n2), std::swap(s1, s2);
+    if (n1 == 1 || s2 >= (n1 - 1) * s1 + len || s1 >= (n2 - 1) * s2 + len) return false;
+    for (int64_t k = 1; k < n1; ++k) {
+        const int64_t l = std::min(k * s1 / s2, n2 - 1), past = k * s1 - l * s2;
+        if (past < len || (l + 1 < n2 && s2 - past < len)) return true;
+    }
+    return false;
+}
+
 // rows of an operand, and whether all of them are 16-byte aligned
 pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, int tokens, int heads, bool out, bool& vec) {
     const int size = dtype_size(dtype);
@@ -427,8 +439,9 @@ pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, 
     CHECK(r->token_stride >= 0 && r->head_stride >= 0 && r->token_stride < ((int64_t)1 << 40) &&
               r->head_stride < ((int64_t)1 << 40),
           PI_ERR_SHAPE, "%s: strides must be in 0..2^40", name);
-    CHECK(!out || ((tokens == 1 || r->token_stride >= d) && (heads == 1 || r->head_stride >= d)), PI_ERR_SHAPE,
-          "%s: rows that are written may not overlap", name);
+    CHECK(!out || ((tokens == 1 || r->token_stride >= d) && (heads == 1 || r->head_stride >= d) &&
+                   !rows_collide(tokens, r->token_stride, heads, r->head_stride, d)),
+          PI_ERR_SHAPE, "%s: rows that are written may not overlap", name);
     vec = vec && aligned(r->data, 16) && (tokens == 1 || r->token_stride * size % 16 == 0) &&
           (heads == 1 || r->head_stride * size % 16 == 0);
     return PI_OK;

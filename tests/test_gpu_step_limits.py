@@ -58,3 +58,20 @@ def test_norm_of_tiny_weights_is_rounded_once(off, d, form):
     codes, want = host(mx._keep[0]), R.packed(R.codes(y, form), form)
     assert np.array_equal(host(mx._keep[1]), R.scales(y, form))
     assert int((codes != want).sum()) == 0
+
+
+@pytest.mark.parametrize("tokens,heads,token_stride,head_stride", [(5, 4, 1, 5), (5, 4, 4, 1), (3, 3, 2, 3), (2, 3, 7, 2), (4, 2, 2, 5)])
+def test_norm_writes_rows_in_any_order(tokens, heads, token_stride, head_stride):
+    """Rows that lie between each other without meeting, and what lies between them."""
+    d = 64
+    rng = np.random.default_rng(tokens)
+    x = rng.standard_normal((tokens, heads, d)).astype(np.float32)
+    flat = torch.full((40 * d,), 7.0, device="cuda")
+    y = flat.as_strided((tokens, heads, d), (token_stride * d, head_stride * d, 1))
+    pb.pi_rms_norm(pb.make_norm(None, d=d), dev(x), y=y)
+    torch.cuda.synchronize()
+    want = R.norm(x, None, 1e-5)
+    assert (np.abs(host(y) - want) <= 2.0 ** -22 * np.abs(want)).all()
+    places = {i * token_stride + j * head_stride for i in range(tokens) for j in range(heads)}
+    assert len(places) == tokens * heads
+    assert all(bool((flat[p * d:(p + 1) * d] == 7).all()) for p in range(40) if p not in places)
