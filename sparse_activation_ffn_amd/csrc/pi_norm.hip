@@ -439,9 +439,8 @@ pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, 
     CHECK(r->token_stride >= 0 && r->head_stride >= 0 && r->token_stride < ((int64_t)1 << 40) &&
               r->head_stride < ((int64_t)1 << 40),
           PI_ERR_SHAPE, "%s: strides must be in 0..2^40", name);
-    CHECK(!out || ((tokens == 1 || r->token_stride >= d) && (heads == 1 || r->head_stride >= d) &&
-                   !rows_collide(tokens, r->token_stride, heads, r->head_stride, d)),
-          PI_ERR_SHAPE, "%s: rows that are written may not overlap", name);
+    CHECK(!out || ((tokens == 1 || r->token_stride >= d) && (heads == 1 || r->head_stride >= d)), PI_ERR_SHAPE,
+          "%s: rows that are written may not overlap", name);
     vec = vec && aligned(r->data, 16) && (tokens == 1 || r->token_stride * size % 16 == 0) &&
           (heads == 1 || r->head_stride * size % 16 == 0);
     return PI_OK;
@@ -520,6 +519,8 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
         TRY(check_in_place(out, name, dtype, x, dtype, tokens, heads));
         TRY(check_in_place(out, name, dtype, delta, ddtype, tokens, heads));
         TRY(check_apart(out, name, dtype, mx, d, tokens, heads));
+        CHECK(!out || !rows_collide(tokens, out->token_stride, heads, out->head_stride, d), PI_ERR_SHAPE,
+              "norm: %s has rows that overlap", name);
     }
     TRY(check_apart(x, "x", dtype, mx, d, tokens, heads));
     TRY(check_apart(delta, "delta", ddtype, mx, d, tokens, heads));
