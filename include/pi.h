@@ -715,8 +715,11 @@ typedef struct pi_norm {
  * At least one of sum, y and mx; sum only with delta.  A hidden state without heads
  * has heads = 1.  Rows need not be 16-byte aligned here: an element's alignment
  * does (rows and strides of 16 bytes are faster).  sum and y may each be x or
- * delta itself (same rows, same type: refused otherwise), but not each other; they may
- * overlap neither in another way, and mx none of them.  The mean is summed in 64 bits.
+ * delta itself (same rows, same type), but not each other; they may overlap neither in
+ * another way, and mx none of them: all of that is refused.  Rows that lie between
+ * those of another operand are told from overlapping ones where both have the same
+ * strides, or a token's heads of one lie between those of the other; with other strides
+ * an output that reaches into an operand's memory is refused.  The mean is summed in 64 bits.
  * An infinity or a NaN in a row reaches the row's outputs as the formula says.
  * tokens * heads is at most 2^23, for d > 2048 at most 2^21.
  * One kernel, no workspace.

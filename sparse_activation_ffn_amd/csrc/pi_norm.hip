@@ -431,6 +431,42 @@ bool rows_collide(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len) {
     return false;
 }
 
+// An operand's rows, in bytes.
+struct Place {
+    int64_t at, ts, hs, len;
+    Place(const pi_rows* r, int dtype, int d, int tokens, int heads)
+        : at((int64_t)(uintptr_t)r->data), ts(tokens > 1 ? r->token_stride * dtype_size(dtype) : 0),
+          hs(heads > 1 ? r->head_stride * dtype_size(dtype) : 0), len((int64_t)d * dtype_size(dtype)) {}
+};
+
+// Whether rows of two operands may share memory.  Where both have the same strides, rows that lie between each other are told
+// from rows that meet: as above, for every k the l's that can bring two rows together.  Where the strides of the heads alone
+// differ, so are the heads of every token of one that lie between those of the other.
+bool rows_may_meet(const Place& p, const Place& q, int64_t tokens, int64_t heads) {
+    const int64_t size_p = (heads - 1) * p.hs + p.len, size_q = (heads - 1) * q.hs + q.len;   // of a token
+    if (p.at + (tokens - 1) * p.ts + size_p <= q.at || q.at + (tokens - 1) * q.ts + size_q <= p.at) return false;
+    if (p.ts != q.ts) return true;
+    const int64_t apart = q.at - p.at;
+    if (p.hs != q.hs) {
+        if (p.ts == 0) return true;
+        const int64_t in_token = (apart % p.ts + p.ts) % p.ts;
+        return in_token < size_p || in_token + size_q > p.ts;
+    }
+    int64_t n1 = tokens, s1 = p.ts, n2 = heads, s2 = p.hs;
+    if (n1 > n2) std::swap(n1, n2), std::swap(s1, s2);
+    for (int64_t k = 1 - n1; k < n1; ++k) {
+        const int64_t from = apart + k * s1;
+        // the lowest l for which q's row ends past p's beginning
+        int64_t l = 1 - n2;
+        if (s2 > 0) {
+            const int64_t past = -q.len - from;                              // l s2 > past
+            l = std::max(l, past >= 0 ? past / s2 + 1 : -((-past - 1) / s2));
+        }
+        if (l < n2 && from + l * s2 < p.len && from + l * s2 > -q.len) return true;
+    }
+    return false;
+}
+
 // rows of an operand, and whether all of them are 16-byte aligned
 pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, int tokens, int heads, bool out, bool& vec) {
     const int size = dtype_size(dtype);
@@ -439,6 +475,8 @@ pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, 
     CHECK(r->token_stride >= 0 && r->head_stride >= 0 && r->token_stride < ((int64_t)1 << 40) &&
               r->head_stride < ((int64_t)1 << 40),
           PI_ERR_SHAPE, "%s: strides must be in 0..2^40", name);
+    CHECK((tokens - 1) * r->token_stride + (heads - 1) * r->head_stride < (int64_t)1 << 56, PI_ERR_SHAPE,
+          "%s: rows past what addresses reach", name);
     CHECK(!out || ((tokens == 1 || r->token_stride >= d) && (heads == 1 || r->head_stride >= d)), PI_ERR_SHAPE,
           "%s: rows that are written may not overlap", name);
     vec = vec && aligned(r->data, 16) && (tokens == 1 || r->token_stride * size % 16 == 0) &&
@@ -446,12 +484,18 @@ pi_status check_norm_rows(const pi_rows* r, const char* name, int dtype, int d, 
     return PI_OK;
 }
 
-// an output that begins where an input does takes its place: the same rows, of the same type
-pi_status check_in_place(const pi_rows* out, const char* name, int dtype, const pi_rows* in, int in_dtype, int tokens, int heads) {
-    if (!out || !in || out->data != in->data) return PI_OK;
-    CHECK(dtype == in_dtype && (tokens == 1 || out->token_stride == in->token_stride) &&
-              (heads == 1 || out->head_stride == in->head_stride),
-          PI_ERR_ARG, "norm: %s takes an input's place with other rows or another type", name);
+// an output takes an input's place with the same rows, of the same type; it may not overlap an operand in another way
+pi_status check_in_place(const pi_rows* out, const char* name, int dtype, const pi_rows* in, const char* in_name, int in_dtype, int d,
+                         int tokens, int heads) {
+    if (!out || !in) return PI_OK;
+    if (out->data == in->data) {
+        CHECK(dtype == in_dtype && (tokens == 1 || out->token_stride == in->token_stride) &&
+                  (heads == 1 || out->head_stride == in->head_stride),
+              PI_ERR_ARG, "norm: %s takes the place of %s with other rows or another type", name, in_name);
+        return PI_OK;
+    }
+    CHECK(!rows_may_meet(Place(out, dtype, d, tokens, heads), Place(in, in_dtype, d, tokens, heads), tokens, heads), PI_ERR_ARG,
+          "norm: %s overlaps %s", name, in_name);
     return PI_OK;
 }
 
@@ -516,12 +560,13 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
     }
     for (const pi_rows* out : {sum, y}) {
         const char* name = out == sum ? "sum" : "y";
-        TRY(check_in_place(out, name, dtype, x, dtype, tokens, heads));
-        TRY(check_in_place(out, name, dtype, delta, ddtype, tokens, heads));
+        TRY(check_in_place(out, name, dtype, x, "x", dtype, d, tokens, heads));
+        TRY(check_in_place(out, name, dtype, delta, "delta", ddtype, d, tokens, heads));
         TRY(check_apart(out, name, dtype, mx, d, tokens, heads));
         CHECK(!out || !rows_collide(tokens, out->token_stride, heads, out->head_stride, d), PI_ERR_SHAPE,
               "norm: %s has rows that overlap", name);
     }
+    TRY(check_in_place(sum, "sum", dtype, y, "y", dtype, d, tokens, heads));   // (not in one place: see above)
     TRY(check_apart(x, "x", dtype, mx, d, tokens, heads));
     TRY(check_apart(delta, "delta", ddtype, mx, d, tokens, heads));
     if (mx) a.format = mx->format, a.codes = (uint8_t*)mx->codes, a.scales = mx->scales;

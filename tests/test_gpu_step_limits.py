@@ -75,3 +75,25 @@ def test_norm_writes_rows_in_any_order(tokens, heads, token_stride, head_stride)
     places = {i * token_stride + j * head_stride for i in range(tokens) for j in range(heads)}
     assert len(places) == tokens * heads
     assert all(bool((flat[p * d:(p + 1) * d] == 7).all()) for p in range(40) if p not in places)
+
+
+# places of x and y in rows of ten heads: first head, and heads from one to the next
+@pytest.mark.parametrize("x_at,y_at", [((0, 1), (3, 1)), ((0, 1), (7, 1)), ((1, 2), (0, 2)), ((0, 2), (5, 2)), ((0, 3), (8, 1)),
+                                       ((4, 1), (0, 2))])
+def test_norm_between_the_rows_of_its_input(x_at, y_at):
+    """Heads of a fused row normed into other heads of the same rows."""
+    tokens, heads, d = 6, 3, 64
+    if y_at == (8, 1) or x_at == (4, 1):
+        heads = 2
+    rng = np.random.default_rng(x_at)
+    before = rng.standard_normal((tokens, 10, d)).astype(np.float16)
+    fused = dev(before)
+    x, y = (fused[:, at:at + (heads - 1) * step + 1:step] for at, step in (x_at, y_at))
+    want = R.norm(before[:, x_at[0]::x_at[1]][:, :heads], None, 1e-5)
+    pb.pi_rms_norm(pb.make_norm(None, d=d), x, y=y)
+    torch.cuda.synchronize()
+    after = host(fused)
+    places = [y_at[0] + i * y_at[1] for i in range(heads)]
+    assert (np.abs(after[:, places] - want) <= 2.0 ** -10.9 * np.abs(want) + 2.0 ** -25).all()
+    rest = [i for i in range(10) if i not in places]
+    assert np.array_equal(after[:, rest], before[:, rest])

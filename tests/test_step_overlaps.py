@@ -19,3 +19,42 @@ def test_norm_refuses_rows_written_over_each_other(L, tokens, heads, token_strid
     for dtype in (pb.PI_F16, pb.PI_F32):
         assert _norm(L, tokens=tokens, heads=heads, dtype=dtype, y=rows) == pb.PI_ERR_SHAPE
         assert _norm(L, tokens=tokens, heads=heads, dtype=dtype, y=None, sum_out=rows, delta=_rows()) == pb.PI_ERR_SHAPE
+
+
+# x: 4 tokens of 128 f16 elements from FAR on, 256 bytes a row
+SHIFTED = [_rows(FAR + 2), _rows(FAR - 2), _rows(FAR + 256), _rows(FAR - 256), _rows(FAR + 1022), _rows(FAR - 1022),
+           _rows(FAR + 16, 256), _rows(FAR - 600, 512)]
+
+
+@pytest.mark.parametrize("at", range(len(SHIFTED)))
+def test_norm_refuses_outputs_that_begin_inside_an_operand(L, at):  # noqa: F811
+    """Over x, over delta and over the other output, by an element, a row or the last element."""
+    rows, x = SHIFTED[at], _rows(FAR)
+    away = [_rows(FAR << 1), _rows(FAR << 2)]
+    for kw in (dict(x=x, y=rows), dict(x=x, y=rows, delta=away[0]), dict(x=x, y=None, sum_out=rows, delta=away[0]),
+               dict(x=away[0], delta=x, y=rows), dict(x=away[0], delta=x, y=away[1], sum_out=rows),
+               dict(x=away[0], delta=away[1], y=x, sum_out=rows), dict(x=away[0], delta=away[1], y=rows, sum_out=x)):
+        assert _norm(L, **kw) == pb.PI_ERR_ARG, kw
+
+
+@pytest.mark.parametrize("ddtype", [pb.PI_F16, pb.PI_F32])
+def test_norm_refuses_outputs_between_an_operands_rows(L, ddtype):  # noqa: F811
+    """Heads of 64 f16 elements (128 bytes) in rows of ten heads: x takes heads 0 to 3."""
+    head = 128
+    x, away = _rows(FAR, 640, 64), _rows(FAR << 2, 256, 64)
+    # head 3 of the same token, head 9 and thus head 0 of the next one, half a head; two heads apart from heads one apart
+    for y in (_rows(FAR + 3 * head, 640, 64), _rows(FAR + 9 * head, 640, 64), _rows(FAR - head, 640, 64), _rows(FAR + 7 * head, 640, 64),
+              _rows(FAR + 4 * head - 2, 640, 64), _rows(FAR + 2 * head, 640, 128), _rows(FAR + 640 * 2 * 2 + 2, 640, 64),
+              _rows(FAR + 8 * head, 640, 128), _rows(FAR + 4 * head, 768, 64)):
+        assert _norm(L, d=64, heads=4, x=x, y=y, delta=away, ddtype=ddtype) == pb.PI_ERR_ARG
+        if ddtype == pb.PI_F16:
+            assert _norm(L, d=64, heads=4, x=away, y=y, delta=x) == pb.PI_ERR_ARG
+    # a delta of float32 rows, 256 bytes each in rows of 5 x 256: y among them
+    for y in (_rows(FAR + 3 * 256, 640, 64), _rows(FAR + 4 * 256, 640, 128), _rows(FAR + 254, 640, 128)):
+        assert _norm(L, d=64, heads=4, x=away, y=y, delta=_rows(FAR, 320, 64), ddtype=pb.PI_F32) == pb.PI_ERR_ARG
+
+
+def test_norm_refuses_rows_past_addresses(L):  # noqa: F811
+    far = _rows(FAR, 1 << 39)
+    for kw in (dict(x=far, y=_rows()), dict(y=far), dict(delta=far), dict(sum_out=far, y=None, delta=_rows())):
+        assert _norm(L, tokens=1 << 18, **kw) == pb.PI_ERR_SHAPE
