@@ -719,7 +719,8 @@ typedef struct pi_norm {
  * another way, and mx none of them: all of that is refused.  Rows that lie between
  * those of another operand are told from overlapping ones where both have the same
  * strides, or a token's heads of one lie between those of the other; with other strides
- * an output that reaches into an operand's memory is refused.  The mean is summed in 64 bits.
+ * an output that reaches into an operand's memory is refused, and so is one whose rows or
+ * what lies between them reach into the weight.  The mean is summed in 64 bits.
  * An infinity or a NaN in a row reaches the row's outputs as the formula says.
  * tokens * heads is at most 2^23, for d > 2048 at most 2^21.
  * One kernel, no workspace.

@@ -569,6 +569,17 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
     TRY(check_in_place(sum, "sum", dtype, y, "y", dtype, d, tokens, heads));   // (not in one place: see above)
     TRY(check_apart(x, "x", dtype, mx, d, tokens, heads));
     TRY(check_apart(delta, "delta", ddtype, mx, d, tokens, heads));
+    if (norm->weight) {
+        const int64_t bytes = (int64_t)d * dtype_size(norm->wdtype);
+        // (a weight between two rows of an output is refused as well)
+        for (const pi_rows* out : {sum, y}) {
+            if (!out) continue;
+            const Place p(out, dtype, d, tokens, heads);
+            CHECK(apart(out->data, (tokens - 1) * p.ts + (heads - 1) * p.hs + p.len, norm->weight, bytes), PI_ERR_ARG,
+                  "norm: %s overlaps the weight", out == sum ? "sum" : "y");
+        }
+        CHECK(!mx || apart(norm->weight, bytes, mx), PI_ERR_ARG, "norm: mx overlaps the weight");
+    }
     if (mx) a.format = mx->format, a.codes = (uint8_t*)mx->codes, a.scales = mx->scales;
     if (norm->weight) a.wdtype = norm->wdtype, a.weight = (const uint8_t*)norm->weight;
     a.eps = norm->eps;

@@ -58,3 +58,16 @@ def test_norm_refuses_rows_past_addresses(L):  # noqa: F811
     far = _rows(FAR, 1 << 39)
     for kw in (dict(x=far, y=_rows()), dict(y=far), dict(delta=far), dict(sum_out=far, y=None, delta=_rows())):
         assert _norm(L, tokens=1 << 18, **kw) == pb.PI_ERR_SHAPE
+
+
+@pytest.mark.parametrize("wdtype,size", [(pb.PI_F16, 2), (pb.PI_F32, 4)])
+def test_norm_refuses_outputs_over_its_weight(L, wdtype, size):  # noqa: F811
+    at = FAR
+    kw = dict(weight=at, wdtype=wdtype)
+    for rows in (_rows(at), _rows(at - 1022), _rows(at + 128 * size - 2), _rows(at - 256 * 3 + 2), _rows(at - 2048 + 128, 1024)):
+        assert _norm(L, y=rows, **kw) == pb.PI_ERR_ARG
+        assert _norm(L, y=None, sum_out=rows, delta=_rows(FAR << 1), **kw) == pb.PI_ERR_ARG
+    # 4 x 128 codes and 4 x 4 scales
+    for m in (_mx(codes=at, scales=FAR << 1), _mx(codes=at - 496, scales=FAR << 1), _mx(codes=at + 128 * size - 16, scales=FAR << 1),
+              _mx(codes=FAR << 1, scales=at), _mx(codes=FAR << 1, scales=at + 128 * size - 16)):
+        assert _norm(L, y=None, mx=m, **kw) == pb.PI_ERR_ARG
