@@ -684,7 +684,8 @@ pi_status pi_pages_copy(const pi_kv_cache* cache, const int32_t* src, const int3
  *   PI_MXFP4: codes [rows][cols / 2]: element 2i in the low nibble of byte i,
  *             2i + 1 in the high one; sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
  *             1, 1.5, 2, 3, 4, 6
- * codes and scales ([rows][cols / 32]) are contiguous and 16-byte aligned. */
+ * codes and scales ([rows][cols / 32]) are contiguous and 16-byte aligned; of a matrix
+ * that a call writes they may not overlap. */
 enum { PI_MXFP8 = 0, PI_MXFP4 = 1 };
 typedef struct pi_mx {
     int32_t format;       /* PI_MXFP8 or PI_MXFP4 */

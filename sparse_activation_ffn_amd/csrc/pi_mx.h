@@ -39,6 +39,13 @@ inline bool apart(const void* p, int64_t bytes, const pi_mx* m) {
            apart(p, bytes, m->scales, (int64_t)m->rows * (m->cols / 32));
 }
 
+// codes and scales of a matrix that is written
+inline pi_status check_written(const pi_mx* m, const char* name) {
+    CHECK(apart(m->codes, m->rows * mx_row_bytes(m->format, m->cols), m->scales, (int64_t)m->rows * (m->cols / 32)), PI_ERR_ARG,
+          "%s: codes and scales overlap", name);
+    return PI_OK;
+}
+
 inline pi_status check_elem_dtype(int dtype, const char* name) {
     CHECK(dtype == PI_F32 || dtype == PI_F16, PI_ERR_DTYPE, "%s: dtype must be PI_F32 or PI_F16", name);
     return PI_OK;

@@ -567,6 +567,7 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
               "norm: %s has rows that overlap", name);
     }
     TRY(check_in_place(sum, "sum", dtype, y, "y", dtype, d, tokens, heads));   // (not in one place: see above)
+    if (mx) TRY(check_written(mx, "mx"));
     TRY(check_apart(x, "x", dtype, mx, d, tokens, heads));
     TRY(check_apart(delta, "delta", ddtype, mx, d, tokens, heads));
     if (norm->weight) {
@@ -589,6 +590,7 @@ pi_status pi_rms_norm(const pi_norm* norm, int32_t tokens, int32_t heads, int32_
 
 pi_status pi_mx_quantize(const void* x, int64_t row_stride, int32_t dtype, const pi_mx* mx, void* stream) {
     TRY(check_matrix(x, row_stride, dtype, mx, "x", false));
+    TRY(check_written(mx, "mx"));
     return mx->rows == 0 ? PI_OK : convert<true>(x, row_stride, dtype, mx, (hipStream_t)stream);
 }
 

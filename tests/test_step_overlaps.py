@@ -71,3 +71,15 @@ def test_norm_refuses_outputs_over_its_weight(L, wdtype, size):  # noqa: F811
     for m in (_mx(codes=at, scales=FAR << 1), _mx(codes=at - 496, scales=FAR << 1), _mx(codes=at + 128 * size - 16, scales=FAR << 1),
               _mx(codes=FAR << 1, scales=at), _mx(codes=FAR << 1, scales=at + 128 * size - 16)):
         assert _norm(L, y=None, mx=m, **kw) == pb.PI_ERR_ARG
+
+
+@pytest.mark.parametrize("fmt,size", [(pb.PI_MXFP8, 512), (pb.PI_MXFP4, 256)])
+def test_codes_and_scales_that_are_written_lie_apart(L, fmt, size):  # noqa: F811
+    """4 x 128 codes and 16 scales: at the same place, at the last codes, and the other way round."""
+    for scales in (FAR, FAR + 16, FAR + size - 16):
+        m = _mx(format=fmt, codes=FAR, scales=scales)
+        assert L.pi_mx_quantize(FAR << 1, 128, pb.PI_F16, ref(m), None) == pb.PI_ERR_ARG
+        assert _norm(L, y=None, mx=m) == pb.PI_ERR_ARG
+    wide = _mx(format=fmt, rows=64, codes=FAR, scales=FAR - 16)          # 256 scales
+    assert L.pi_mx_quantize(FAR << 1, 128, pb.PI_F16, ref(wide), None) == pb.PI_ERR_ARG
+    assert _norm(L, tokens=64, y=None, mx=wide) == pb.PI_ERR_ARG
