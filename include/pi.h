@@ -797,7 +797,8 @@ typedef struct pi_sample_rule {
  *   kept   [rows] int32, out, or NULL: how many tokens the rules keep
  * Weights are formed in 64 bits and summed as integers of 2^-43: the result depends on
  * no order of sums (a token below 2^-44 of the first is kept, but never drawn).
- * token, prob and kept may overlap neither each other nor what the call reads.
+ * token, prob and kept may overlap neither each other nor what the call reads, and
+ * the workspace none of these.
  * rows 0..65535, vocab 1..2^20.  Needs a workspace of pi_sample_workspace_bytes: 63 KB a
  * row (256-byte aligned).
  * A row in which more than 4096 tokens lie near the border of top-k or top-p (equal

@@ -927,6 +927,9 @@ pi_status pi_sample(const void* logits, int32_t rows, int32_t vocab, int64_t row
         for (const void* in : ins) free = free && apart(outs[i], list, in, list);
         CHECK(free, PI_ERR_ARG, "sample: token, prob and kept may overlap neither each other nor what the call reads");
     }
+    bool free = apart(ws, sample_bytes(rows, vocab), logits, span);
+    for (const void* in : ins) free = free && apart(ws, sample_bytes(rows, vocab), in, list);
+    CHECK(free, PI_ERR_ARG, "sample: the workspace overlaps what the call reads");
     SampleArgs a{(const uint8_t*)logits, row_stride, rule->temperature, rule->top_k, rule->top_p, rule->min_p, u, token, prob,
                  kept, rows, vocab, 0, 0, 0, (uint8_t*)ws, WS_ROW};
     chunks_of(a);

@@ -83,3 +83,15 @@ def test_codes_and_scales_that_are_written_lie_apart(L, fmt, size):  # noqa: F81
     wide = _mx(format=fmt, rows=64, codes=FAR, scales=FAR - 16)          # 256 scales
     assert L.pi_mx_quantize(FAR << 1, 128, pb.PI_F16, ref(wide), None) == pb.PI_ERR_ARG
     assert _norm(L, tokens=64, y=None, mx=wide) == pb.PI_ERR_ARG
+
+
+def test_sample_refuses_a_workspace_over_what_it_reads(L):  # noqa: F811
+    need = L.pi_sample_workspace_bytes(2, 1000)
+    at = [FAR * i for i in range(1, 10)]                             # logits, four lists, u, token, prob, kept
+
+    def call(ws):
+        rule = pb.SampleRule(*at[1:5])
+        return L.pi_sample(at[0], 2, 1000, 1000, pb.PI_F16, ref(rule), at[5], at[6], at[7], at[8], ws, need, None)
+    for operand in at:
+        assert call(operand) == call(operand - (need - 4) // 256 * 256) == pb.PI_ERR_ARG
+    assert call(at[0] + 3840) == pb.PI_ERR_ARG                       # the last of 2 x 1000 f16 logits
