@@ -763,7 +763,7 @@ pi_status pi_mx_dequantize(const pi_mx* mx, void* out, int64_t row_stride, int32
  * Refused (PI_ERR_SHAPE) past 2^23 tiles of 128 x 128 outputs.
  * Needs a workspace of pi_mx_product_workspace_bytes(m, n, k) bytes for m = a->rows,
  * n = w->rows, k = cols (256-byte aligned; 0 bytes: none; a call with fewer rows of a
- * needs no more than one with more).
+ * needs no more than one with more), which may overlap nothing else of the call's.
  */
 size_t pi_mx_product_workspace_bytes(int32_t m, int32_t n, int32_t k);
 pi_status pi_mx_product(const pi_mx* a, const pi_mx* w, const float* bias, void* out,

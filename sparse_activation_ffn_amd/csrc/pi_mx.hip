@@ -723,6 +723,8 @@ pi_status pi_mx_product(const pi_mx* a, const pi_mx* w, const float* bias, void*
     CHECK(apart(out, span, a) && apart(out, span, w) && apart(out, span, bias, (int64_t)w->rows * 4) &&
               apart(out, span, need ? ws : nullptr, need),
           PI_ERR_ARG, "out overlaps what the call reads");
+    CHECK(!need || (apart(ws, need, a) && apart(ws, need, w) && apart(ws, need, bias, (int64_t)w->rows * 4)), PI_ERR_ARG,
+          "the workspace overlaps what the call reads");
     const bool vec = aligned(out, 4 * size) && (a->rows == 1 || out_stride % 4 == 0);
     ProductArgs p{(const uint8_t*)a->codes, a->scales, (const uint8_t*)w->codes, w->scales, bias, (uint8_t*)out, out_stride,
                   a->rows, w->rows, a->cols, plan.splits, (float*)ws, vec};

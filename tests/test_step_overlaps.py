@@ -95,3 +95,14 @@ def test_sample_refuses_a_workspace_over_what_it_reads(L):  # noqa: F811
     for operand in at:
         assert call(operand) == call(operand - (need - 4) // 256 * 256) == pb.PI_ERR_ARG
     assert call(at[0] + 3840) == pb.PI_ERR_ARG                       # the last of 2 x 1000 f16 logits
+
+
+def test_product_refuses_a_workspace_over_what_it_reads(L):  # noqa: F811
+    at = [FAR * 64 * i for i in range(1, 7)]                         # codes and scales of a and of w, bias, out
+    a, w = _mx(rows=48, cols=8192, codes=at[0], scales=at[1]), _mx(format=pb.PI_MXFP4, rows=256, cols=8192, codes=at[2], scales=at[3])
+    need = L.pi_mx_product_workspace_bytes(48, 256, 8192)
+    assert need and need % 256 == 0
+    sizes = (48 * 8192, 48 * 256, 256 * 4096, 256 * 256, 1024)
+    for operand, size in zip(at, sizes):
+        for ws in (operand, operand - need + 256, operand + size - 256):
+            assert L.pi_mx_product(ref(a), ref(w), at[4], at[5], 256, pb.PI_F32, ws, need, None) == pb.PI_ERR_ARG
