@@ -653,7 +653,10 @@ ProductPlan plan_product(int64_t m, int64_t n, int64_t k) {
     // Tiles of 128 x 256 take four fifths of the time of two of 128 x 128, where there are enough (4096 x 10240 x 8192: 282
     // us and 358; 1024 x 8192 x 8192, 256 of them: 80 and 77; 512 x 8192 x 8192, 128 of them: 78 and 53).
     if (form == TILE_128 && (m + 127) / 128 * ((n + 255) / 256) > 256) return {TILE_WIDE, 1};
-    const int64_t splits = std::max<int64_t>(1, std::min(256 / tiles, k / (2 * LONG)));
+    const int64_t most = std::max<int64_t>(1, std::min(256 / tiles, k / (2 * LONG)));
+    // (Every split takes as many pieces of 512, so that fewer of them may do: 5 for 16 pieces are 4 with four each.  One that
+    // is left without any adds zeros that the join has to read: 256 x 1408 x 12288, 11 and 8 splits, 21.5 and 20.0 us.)
+    const int64_t pieces = (k + LONG - 1) / LONG, each = (pieces + most - 1) / most, splits = (pieces + each - 1) / each;
     // Sixteen rows or fewer: one wave per 16 rows of w and eighth of K where tiles of 64 rows of w are too few, without a
     // join (us, and tiles: 1 x 1024 x 8192 5.4, 10.6; 1 x 4096 6.5, 10.5; 1 x 8192 11.7, 11.8; 1 x 10240 14.5, 12.4).
     if (form == TILE_16) return {tiles < 128 ? WAVES_SHARE_K : TILE_16, 1};
