@@ -754,8 +754,10 @@ pi_status pi_mx_dequantize(const pi_mx* mx, void* out, int64_t row_stride, int32
  * NULL.  out: rows out_stride elements apart (>= w->rows, an element's alignment),
  * PI_F32 or PI_F16; it may overlap nothing that the call reads.
  * Sums are float32, out is rounded once.  Products are exact, but: with a in PI_MXFP8
- * and out in PI_F32, values of a and w below 2^-126 are first rounded to multiples
- * of 2^-133 (bfloat16's); with a in PI_MXFP8 and out in PI_F16, the matrix
+ * and out in PI_F32, both sides are first turned into bfloat16, where values below 2^-126
+ * are rounded to multiples of 2^-133, and those from 2^128 on are infinite (and NaN
+ * times 0), which takes a scale of 247 or more in a, of 253 or more in w: more than
+ * pi_mx_quantize gives, as float32 has no such values; with a in PI_MXFP8 and out in PI_F16, the matrix
  * instruction cuts the products of eight neighbouring elements (k / 8 the same) 2^-13
  * below the largest of them; outputs are off by some 2^-16 of their usual size, f16's
  * own rounding being 2^-12.  A NaN in a row of a or w reaches the outputs that it takes

@@ -37,8 +37,8 @@ struct ProductArgs {
 //   FP8     a MXFP8: the same instruction.  It cuts the products of eight neighbouring elements 2^-13 below the largest
 //           of them, which leaves outputs off by 2e-5 of their size (measured; activations with outliers): a tenth of
 //           f16's own rounding, so it is taken for f16 outputs alone
-//   FP8_F32 a MXFP8, float32 outputs: both sides turned to bfloat16 with their scales, which is exact down to 2^-126,
-//           and the instruction of 16 x 16 x 32, half as fast
+//   FP8_F32 a MXFP8, float32 outputs: both sides turned to bfloat16 with their scales, which is exact from 2^-126 to below
+//           2^128 (what float32 holds, and so what is quantised from it), and the instruction of 16 x 16 x 32, half as fast
 enum { M_FP4 = 0, M_FP8 = 1, M_FP8_F32 = 2 };
 
 // A fragment: row l % 16 of 16 rows, a part of 128 elements in each lane; g = l / 16.

@@ -140,3 +140,27 @@ def test_nan_and_far_scales(m, n, k, fa, out):
     fine = known & ~nan
     assert (np.abs(want[fine]) < 60000).all()
     assert np.abs(want[0, 1]) > 0.01 and (np.abs(got - want) <= tol)[fine].all()
+
+
+@pytest.mark.parametrize("m,n", [(1, 70), (5, 8200), (20, 70), (40, 70), (70, 70), (2100, 4100)])
+def test_values_at_float32s_end(m, n):
+    """MXFP8 to float32 goes through bfloat16: exact up to the largest values that quantisation gives (448 and 6 times 2^119
+    and 2^125), infinite from 2^128 on.  The f16 form has no such end."""
+    k = 1024
+
+    def product(code, scale, w_code, w_scale, out):
+        a, w = np.zeros((m, k), np.uint8), np.zeros((n, k // 2), np.uint8)
+        sa, sw = np.full((m, k // 32), 127, np.uint8), np.full((n, k // 32), 127, np.uint8)
+        a[:, 515], w[:, 257], sa[:, 16], sw[:, 16] = code, w_code << 4, scale, w_scale
+        got = run_product((a, sa), (w, sw), "fp8", out=out)
+        assert (got == got[0, 0]).all() or np.isnan(got).all()
+        return float(got[0, 0])
+    top, one, two, six, zero = 0x7e, 0x38, 4, 7, 0                       # (448, 1; 2, 6, 0)
+    for out in ("f32", "f16"):
+        assert product(top, 246, two, 5, out) == 448 * 2 * 2.0 ** -3
+        assert product(one, 254, two, 0, out) == 2
+        assert product(one, 7, six, 252, out) == 6 * 2.0 ** 5
+    assert product(top, 247, two, 4, "f32") == product(one, 0, six, 253, "f32") == np.inf
+    assert np.isnan(product(top, 254, zero, 127, "f32")) and np.isnan(product(0, 127, six, 254, "f32"))
+    assert product(top, 247, two, 4, "f16") == 448 * 2 * 2.0 ** -3 and product(one, 0, six, 253, "f16") == 6 * 2.0 ** -1
+    assert product(top, 254, zero, 127, "f16") == product(0, 127, six, 254, "f16") == 0
