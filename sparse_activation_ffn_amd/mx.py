@@ -13,16 +13,18 @@ from . import binding as pb
 
 
 class Scratch:
-    """Device memory that the calls of one stream use in turn.  For one that needs more there is a
-    new piece, a power of two of bytes; the pieces before stay, since a captured graph may name
-    them (all together are less than twice the last)."""
+    """Device memory that the calls of one stream use in turn: as much as the first needs.  For one
+    that needs more there is a new piece, of twice the last one's bytes at least; the pieces before
+    stay, since a captured graph may name them (all together are less than twice the last)."""
 
     def __init__(self):
         self.pieces = []
 
     def bytes(self, need: int, device) -> torch.Tensor:
-        if not self.pieces or self.pieces[-1].numel() < need:
-            self.pieces.append(torch.empty(max(256, 1 << (need - 1).bit_length()), dtype=torch.uint8, device=device))
+        last = self.pieces[-1].numel() if self.pieces else 0
+        if last < max(need, 1):
+            size = max(-(-need // 256) * 256, 2 * last, 256)
+            self.pieces.append(torch.empty(size, dtype=torch.uint8, device=device))
         return self.pieces[-1]
 
 
