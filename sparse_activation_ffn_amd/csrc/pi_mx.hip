@@ -147,30 +147,21 @@ __device__ __forceinline__ void store_out(const ProductArgs& p, int i, int j, fl
 
 constexpr int LONG = 512;        // elements whose scales come in one load
 
-// The elements from `from` on, past the last whole 512: fragments straight from memory, in steps of 128.
-template <int MODE, int MT, int NT>
+// The elements past the last whole 512: fragments straight from memory, in steps of 128.
+template <int MODE>
 __device__ __forceinline__ void tail_steps(const ProductArgs& p, const uint8_t* w, const uint8_t* ws, const uint8_t* a,
-                                           const uint8_t* as, const unsigned (&w_row)[NT], const unsigned (&a_row)[MT], int g,
-                                           f4 (&sum)[MT][NT]) {
+                                           const uint8_t* as, unsigned w_row, unsigned a_row, int g, f4 (&sum)[1][1]) {
     constexpr bool WIDE = MODE != M_FP4;
     const int wb = p.k / 2, ab = WIDE ? p.k : p.k / 2, sb = p.k / 32;
     for (int k = p.k / LONG * LONG; k < p.k; k += 128) {
-        const bool cut = k + 128 > p.k;
-        Frag<false> wf[NT];
-        int wsc[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            wf[j] = load_frag<MODE, false, false>(w, w_row[j] * wb, k, p.k, g);
-            wsc[j] = load_scale(ws, w_row[j] * sb, k, p.k, g);
-            if (cut) clear_tail<MODE, false>(wf[j], wsc[j], k, p.k, g);
+        Frag<false> wf[1] = {load_frag<MODE, false, false>(w, w_row * wb, k, p.k, g)};
+        Frag<WIDE> af[1] = {load_frag<MODE, WIDE, false>(a, a_row * ab, k, p.k, g)};
+        int wsc[1] = {load_scale(ws, w_row * sb, k, p.k, g)}, asc[1] = {load_scale(as, a_row * sb, k, p.k, g)};
+        if (k + 128 > p.k) {
+            clear_tail<MODE, false>(wf[0], wsc[0], k, p.k, g);
+            clear_tail<MODE, WIDE>(af[0], asc[0], k, p.k, g);
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            Frag<WIDE> af[1] = {load_frag<MODE, WIDE, false>(a, a_row[i] * ab, k, p.k, g)};
-            int asc[1] = {load_scale(as, a_row[i] * sb, k, p.k, g)};
-            if (cut) clear_tail<MODE, WIDE>(af[0], asc[0], k, p.k, g);
-            steps_of<MODE, 1, NT>(wf, wsc, af, asc, reinterpret_cast<f4(&)[1][NT]>(sum[i]));
-        }
+        steps_of<MODE, 1, 1>(wf, wsc, af, asc, sum);
     }
 }
 
@@ -199,82 +190,54 @@ __device__ __forceinline__ void store_out4(const ProductArgs& p, int i, int j, f
 // ---- few rows of a -----------------------------------------------------------------
 //
 // The weights' bytes bound it: every one is read once, by one wave, from memory into the registers of the matrix
-// instruction, no LDS and no barrier on the way.  A workgroup takes NT x 16 rows of w and 16 of a; its NW waves share out K in
+// instruction, no LDS and no barrier on the way.  A workgroup takes 16 rows of w and 16 of a; its KW waves share out K in
 // pieces of 512 elements and join their sums in LDS in a fixed order.  A piece is what is loaded at once, so that both
 // halves of a 128-byte line are asked for together and a row's scales in one load: in pieces of 128 the lines had left the
 // 32 KB of the first-level cache before their other half was asked for (1 x 10240 x 8192: 18.4 us, 14.5 so).  A load
 // of 16 rows takes the path to memory some 64 cycles whatever it brings, which is why tiles through LDS are faster where
 // there are enough of them; 1 x 4096 x 8192 takes 6.5 us with the launch.
-template <int MODE, int MT, int NT, int STEPS>
+constexpr int STEPS = LONG / 128;
+template <int MODE>
 struct Piece {
-    Frag<false> w[STEPS][NT];
-    Frag<MODE != M_FP4> a[STEPS][MT];
-    int ws[STEPS][NT], as[STEPS][MT];       // 4 scales each
+    Frag<false> w[STEPS][1];
+    Frag<MODE != M_FP4> a[STEPS][1];
+    unsigned ws[STEPS], as[STEPS];          // 4 scales each
 };
 
-// the scales of STEPS times 128 elements of a row, at any alignment
-template <int STEPS>
-__device__ __forceinline__ void load_scales(const uint8_t* base, unsigned off, int* v, int stride) {
-    int t[STEPS];
-    __builtin_memcpy(t, base + off, 4 * STEPS);
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) v[i * stride] = t[i];
-}
-
-template <int MODE, int DT, int MT, int NT, int NG, int KW, int STEPS>
-__global__ __launch_bounds__(WAVE * NG * KW) void k_mx_few(ProductArgs p) {
-    __shared__ f4 parts[KW][NG][MT * NT][WAVE];
+template <int MODE, int DT, int KW>
+__global__ __launch_bounds__(WAVE * KW) void k_mx_few(ProductArgs p) {
+    __shared__ f4 parts[KW][WAVE];
     constexpr bool WIDE = MODE != M_FP4;
-    typedef Piece<MODE, MT, NT, STEPS> P;
     const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), g = lane / 16;
-    const int ng = wave % NG, kw = wave / NG;
-    const int n0 = blockIdx.x * 16 * NT * NG, m0 = blockIdx.y * 16 * MT;
+    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
     const int wb = p.k / 2, ab = WIDE ? p.k : p.k / 2, sb = p.k / 32;   // bytes of a row
     const uint8_t* w = p.w + (int64_t)n0 * wb;
     const uint8_t* a = p.a + (int64_t)m0 * ab;
     const uint8_t* ws = p.w_scales + (int64_t)n0 * sb;
     const uint8_t* as = p.a_scales + (int64_t)m0 * sb;
-    unsigned w_row[NT], a_row[MT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) w_row[i] = min(16 * (ng * NT + i) + lane % 16, p.n - 1 - n0);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) a_row[i] = min(16 * i + lane % 16, p.m - 1 - m0);
-    const int pieces = p.k / LONG * (LONG / 128 / STEPS), each = (pieces + KW - 1) / KW;
-    const int from = min(kw * each, pieces), to = min(from + each, pieces);
+    const unsigned w_row = min(lane % 16, p.n - 1 - n0), a_row = min(lane % 16, p.m - 1 - m0);
+    const int pieces = p.k / LONG, each = (pieces + KW - 1) / KW;
+    const int from = min(wave * each, pieces), to = min(from + each, pieces);
 
-    auto load = [&](P& s, int at) __attribute__((always_inline)) {
-        const int k = at * 128 * STEPS;
+    auto load = [&](Piece<MODE>& s, int at) __attribute__((always_inline)) {
+        const int k = at * LONG;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
+        for (int t = 0; t < STEPS; ++t) s.w[t][0] = load_frag<MODE, false, true>(w, w_row * wb, k + 128 * t, p.k, g);
+        __builtin_memcpy(s.ws, ws + (w_row * sb + k / 32), sizeof(s.ws));     // (at any alignment)
 #pragma unroll
-            for (int t = 0; t < STEPS; ++t) s.w[t][i] = load_frag<MODE, false, true>(w, w_row[i] * wb, k + 128 * t, p.k, g);
-            load_scales<STEPS>(ws, w_row[i] * sb + k / 32, &s.ws[0][i], NT);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int t = 0; t < STEPS; ++t) s.a[t][i] = load_frag<MODE, WIDE, true>(a, a_row[i] * ab, k + 128 * t, p.k, g);
-            load_scales<STEPS>(as, a_row[i] * sb + k / 32, &s.as[0][i], MT);
-        }
+        for (int t = 0; t < STEPS; ++t) s.a[t][0] = load_frag<MODE, WIDE, true>(a, a_row * ab, k + 128 * t, p.k, g);
+        __builtin_memcpy(s.as, as + (a_row * sb + k / 32), sizeof(s.as));
     };
-    f4 sum[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) sum[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto compute = [&](const P& s) __attribute__((always_inline)) {
+    f4 sum[1][1] = {{f4{0.0f, 0.0f, 0.0f, 0.0f}}};
+    auto compute = [&](const Piece<MODE>& s) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
-            int wsc[NT], asc[MT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) wsc[i] = s.ws[t][i] >> (8 * g);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) asc[i] = s.as[t][i] >> (8 * g);
-            steps_of<MODE, MT, NT>(s.w[t], wsc, s.a[t], asc, sum);
+            const int wsc[1] = {(int)(s.ws[t] >> (8 * g))}, asc[1] = {(int)(s.as[t] >> (8 * g))};
+            steps_of<MODE, 1, 1>(s.w[t], wsc, s.a[t], asc, sum);
         }
     };
     if (from < to) {
-        P x, y;
+        Piece<MODE> x, y;
         load(x, from);
         int at = from;
         for (; at + 2 < to; at += 2) {
@@ -291,30 +254,24 @@ __global__ __launch_bounds__(WAVE * NG * KW) void k_mx_few(ProductArgs p) {
             compute(x);
         }
     }
-    if (kw == KW - 1) tail_steps<MODE, MT, NT>(p, w, ws, a, as, w_row, a_row, g, sum);
+    if (wave == KW - 1) tail_steps<MODE>(p, w, ws, a, as, w_row, a_row, g, sum);
     // (a matrix instruction takes every lane: it may not sink below a branch)
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            asm volatile("" : "+v"(sum[i][j]));
-            parts[kw][ng][i * NT + j][lane] = sum[i][j];
-        }
+    asm volatile("" : "+v"(sum[0][0]));
+    parts[wave][lane] = sum[0][0];
     __syncthreads();
-    for (int e = threadIdx.x; e < NG * MT * NT * 256; e += WAVE * NG * KW) {
-        const int tile = e / 256, row = e / 16 % 16, col = e % 16;
+    for (int e = threadIdx.x; e < 256; e += WAVE * KW) {
+        const int row = e / 16, col = e % 16, m = m0 + row, n = n0 + col;
         float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < KW; ++i) v += parts[i][tile / (MT * NT)][tile % (MT * NT)][col / 4 * 16 + row][col % 4];
-        const int m = m0 + tile / NT % MT * 16 + row, n = n0 + (tile / (MT * NT) * NT + tile % NT) * 16 + col;
+        for (int i = 0; i < KW; ++i) v += parts[i][col / 4 * 16 + row][col % 4];
         if (m < p.m && n < p.n) store_out<DT>(p, m, n, v);
     }
 }
 
-template <int MODE, int DT, int MT, int NT, int NG, int KW, int STEPS>
+template <int MODE, int DT, int KW>
 pi_status launch_few(const ProductArgs& p, hipStream_t s) {
-    const dim3 grid((p.n + 16 * NT * NG - 1) / (16 * NT * NG), (p.m + 16 * MT - 1) / (16 * MT)), block(WAVE * NG * KW);
-    return launch(PI_K_MX_PRODUCT, k_mx_few<MODE, DT, MT, NT, NG, KW, STEPS>, grid, block, 0, s, p);
+    const dim3 grid((p.n + 15) / 16, (p.m + 15) / 16), block(WAVE * KW);
+    return launch(PI_K_MX_PRODUCT, k_mx_few<MODE, DT, KW>, grid, block, 0, s, p);
 }
 
 // ---- many rows of a ----------------------------------------------------------------
@@ -671,7 +628,7 @@ template <int MODE, int DT>
 pi_status product(const ProductArgs& p, Form form, hipStream_t s) {
     constexpr bool FP4 = MODE == M_FP4;
     switch (form) {
-        case WAVES_SHARE_K: return launch_few<MODE, DT, 1, 1, 1, 8, 4>(p, s);
+        case WAVES_SHARE_K: return launch_few<MODE, DT, 8>(p, s);
         case TILE_16: return launch_many<MODE, DT, 1, 1, 1, 4, 512, 3>(p, s);
         case TILE_32: return launch_many<MODE, DT, 2, 1, 1, 4, 256, 4>(p, s);
         case TILE_64: return launch_many<MODE, DT, 2, 2, 2, 4, 256, 3>(p, s);
