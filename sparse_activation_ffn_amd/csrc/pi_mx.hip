@@ -195,7 +195,7 @@ __device__ __forceinline__ void store_out4(const ProductArgs& p, int i, int j, f
 // halves of a 128-byte line are asked for together and a row's scales in one load: in pieces of 128 the lines had left the
 // 32 KB of the first-level cache before their other half was asked for (1 x 10240 x 8192: 18.4 us, 14.5 so).  A load
 // of 16 rows takes the path to memory some 64 cycles whatever it brings, which is why tiles through LDS are faster where
-// there are enough of them; 1 x 4096 x 8192 takes 6.5 us with the launch.
+// there are enough of them; 1 x 4096 x 8192 takes 7.0 us with the launch.
 constexpr int STEPS = LONG / 128;
 template <int MODE>
 struct Piece {
@@ -280,8 +280,9 @@ pi_status launch_few(const ProductArgs& p, hipStream_t s) {
 // after it come in by direct loads, which are waited for by count.  A row's 16-byte pieces are permuted by the row, so that the
 // 16 rows that a fragment read takes at one piece lie in 16 different pieces of 256 bytes.  Scales come 512 elements at a time,
 // by direct loads where K is a multiple of 512, else through registers.  The matrix cores bound large products, bytes and the
-// depth of the ring small ones.  us (TFLOP/s), 4096 x 10240 x 8192: MXFP8 to f16 278 (2470), to float32 513 (1340: half the
-// rate, and both sides turned to bfloat16 by every wave that reads them), MXFP4 235 (2930).
+// depth of the ring small ones.  us (TFLOP/s), 4096 x 10240 x 8192: MXFP8 to f16 276 (2490), to float32 488 (1410: half the
+// rate, and both sides turned to bfloat16 by every wave that reads them), MXFP4 224 (3060: there the waves wait 45% of their
+// cycles, for the next stage above all, and LDS is busy for a third).
 __device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
@@ -590,13 +591,13 @@ pi_status launch_many(const ProductArgs& p, hipStream_t s) {
 }
 
 // Which form a product takes.  The chip holds one or two workgroups per unit; forms whose tiles are fewer split K so that
-// each of the 256 units has one, in pieces of 1024 elements at least, and join (a launch of 4 us).  us, MXFP8 to f16, by
-// splits (* what the rule takes):
-//                       1      2      3      4      6
-//   32 x 7168 x 8192    18.4   14.0*  15.4   15.0   17.3
-//   48 x 7168 x 8192    28.4   19.9   17.4   15.3*  21.7
-//   64 x 10240 x 8192   29.7   21.8   20.1*  26.3   26.5
-//   128 x 10240 x 8192  50.9   34.7   30.3*  33.3   33.4
+// each of the 256 units has one, in pieces of 1024 elements at least, and join (a launch of 4 us).  us of MXFP8 to f16, MXFP8
+// to float32 and MXFP4 to f16, weights from memory, by splits (* what the rule takes):
+//                       1               2               3               4               6
+//   32 x 7168 x 8192    18.8 26.3 16.7  14.0 18.0 13.2* 15.3 17.1 14.4  14.7 16.7 13.8  17.2 19.8 15.1
+//   48 x 7168 x 8192    28.7 43.2 24.0  19.7 27.3 17.8  17.3 23.0 15.6  15.2 18.8 14.2* 21.7 27.1 17.8
+//   64 x 10240 x 8192   29.7 43.9 25.5  21.8 29.1 19.8  19.8 25.5 18.4* 26.3 33.4 22.3  26.7 31.5 23.0
+//   128 x 10240 x 8192  51.0 78.2 37.6  34.7 48.5 27.5  30.3 40.7 25.2* 32.8 42.6 28.9  32.7 40.3 30.3
 enum Form { WAVES_SHARE_K, TILE_16, TILE_32, TILE_64, TILE_128, TILE_WIDE };
 struct ProductPlan {
     Form form;
@@ -607,15 +608,18 @@ ProductPlan plan_product(int64_t m, int64_t n, int64_t k) {
     const Form form = m <= 16 ? TILE_16 : m <= 32 ? TILE_32 : m <= 64 ? TILE_64 : TILE_128;
     const int64_t rows = form == TILE_128 ? 128 : 64, cols = form <= TILE_32 ? 64 : 128;
     const int64_t tiles = (m + rows - 1) / rows * ((n + cols - 1) / cols);
-    // Tiles of 128 x 256 take four fifths of the time of two of 128 x 128, where there are enough (4096 x 10240 x 8192: 282
-    // us and 358; 1024 x 8192 x 8192, 256 of them: 80 and 77; 512 x 8192 x 8192, 128 of them: 78 and 53).
+    // Tiles of 128 x 256 take four fifths of the time of two of 128 x 128, where there are enough.  us of 128 x 128 and of
+    // 128 x 256, MXFP8 to f16, to float32, MXFP4: 512 x 8192 x 8192, 128 of them: 54 81 37, 75 127 66; 1024 x 8192 x 8192, 256:
+    // 75 120 52, 77 129 68; 1100 x 8192 x 8192, 288: 111 177 77, 98 183 79; 4096 x 10240 x 8192: 336 566 234, 278 496 228.
     if (form == TILE_128 && (m + 127) / 128 * ((n + 255) / 256) > 256) return {TILE_WIDE, 1};
     const int64_t most = std::max<int64_t>(1, std::min(256 / tiles, k / (2 * LONG)));
     // (Every split takes as many pieces of 512, so that fewer of them may do: 5 for 16 pieces are 4 with four each.  One that
     // is left without any adds zeros that the join has to read: 256 x 1408 x 12288, 11 and 8 splits, 21.5 and 20.0 us.)
     const int64_t pieces = (k + LONG - 1) / LONG, each = (pieces + most - 1) / most, splits = (pieces + each - 1) / each;
     // Sixteen rows or fewer: one wave per 16 rows of w and eighth of K where tiles of 64 rows of w are too few, without a
-    // join (us, and tiles: 1 x 1024 x 8192 5.4, 10.6; 1 x 4096 6.5, 10.5; 1 x 8192 11.7, 11.8; 1 x 10240 14.5, 12.4).
+    // join.  us of waves and of tiles, MXFP8 to f16, to float32, MXFP4 (K = 8192): 1 x 1024 5.9 6.1 5.8, 11.5 15.7 11.7; 1 x 4096
+    // 7.0 7.5 6.1, 11.3 15.8 12.1; 1 x 8192, 128 tiles: 11.5 12.6 9.9, 11.7 16.2 12.9; 1 x 10240 14.6 16.7 14.5, 12.4 16.4 13.6.
+    // (The border is MXFP8 to f16's, whose use is the widest; the other two could go to some 150 tiles.)
     if (form == TILE_16) return {tiles < 128 ? WAVES_SHARE_K : TILE_16, 1};
     return {form, (int)splits};
 }
@@ -634,7 +638,7 @@ pi_status product(const ProductArgs& p, Form form, hipStream_t s) {
         case TILE_64: return launch_many<MODE, DT, 2, 2, 2, 4, 256, 3>(p, s);
         case TILE_128: return launch_many<MODE, DT, 4, 4, 2, 2, FP4 ? 256 : 128, FP4 ? 2 : 3>(p, s);
         default:
-            // (MXFP4, 4096 x 10240 x 8192: 235 us, with 128 x 128 x 256 242, with 256 x 128 x 128 240)
+            // (MXFP4, 4096 x 10240 x 8192, one run: 235 us, with 128 x 128 x 256 242, with 256 x 128 x 128 240)
             if constexpr (MODE == M_FP8_F32)
                 return launch_many<MODE, DT, 8, 4, 1, 4, 128, 2>(p, s);
             else
