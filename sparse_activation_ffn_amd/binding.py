@@ -516,9 +516,10 @@ def pi_mx_product(a: Mx, w: Mx, out, bias=None, ws=None, stream=None):
     pi_mx_product_workspace_bytes(a.rows, w.rows, a.cols) bytes."""
     stride = _matrix("out", out, a.rows, w.rows)
     _vector("bias", bias, "float32", w.rows)
+    room = _workspace(ws)
     device = _on_device((out, bias, ws), a, w)
     _check(lib().pi_mx_product(C.byref(a), C.byref(w), ptr(bias), out.data_ptr(), stride, dtype_code(out), ptr(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream, device)))
+                               room, stream_handle(stream, device)))
 
 
 def pi_sample_workspace_bytes(rows: int, vocab: int) -> int:
@@ -536,10 +537,10 @@ def pi_sample(logits, rule: SampleRule, u, token, prob=None, kept=None, ws=None,
     for t in getattr(rule, "_keep", ()):
         if t is not None and not isinstance(t, int) and t.numel() < rows:
             raise ValueError(f"a rule's list has {t.numel()} entries for {rows} rows")
+    room = _workspace(ws)
     device = _on_device((logits, u, token, prob, kept, ws), rule)
     _check(lib().pi_sample(logits.data_ptr(), rows, vocab, stride, dtype_code(logits), C.byref(rule), ptr(u),
-                           ptr(token), ptr(prob), ptr(kept), ptr(ws),
-                           0 if ws is None else ws.numel() * ws.element_size(), stream_handle(stream, device)))
+                           ptr(token), ptr(prob), ptr(kept), ptr(ws), room, stream_handle(stream, device)))
 
 
 def pi_kernel_timer_start(kid: int, max_launches: int):
@@ -704,6 +705,15 @@ def _norm_rows(name: str, t, shape, dtype):
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has x's dtype")
     return C.byref(Rows(t.data_ptr(), strides[0], strides[1] if len(shape) == 3 else 0))
+
+
+def _workspace(ws) -> int:
+    """Bytes of a workspace (None has none); refuses one whose elements don't lie side by side."""
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.numel() * ws.element_size()
 
 
 def _on_device(tensors, *descriptors) -> int:
