@@ -210,8 +210,8 @@ def ptr(t) -> Optional[int]:
 
 
 def stream_handle(stream=None, device: int = -1) -> Optional[int]:
-    """device: the one that a call's tensors lie on, if that is known: it has to be the current one, on whose streams
-    a call runs."""
+    """device: the one that a call's tensors lie on, if that is known: it has to be the current one, and the stream's
+    (a handle as a number is not looked at)."""
     if stream is None or device >= 0:
         import torch
         here = torch.cuda.current_device()
@@ -221,6 +221,8 @@ def stream_handle(stream=None, device: int = -1) -> Optional[int]:
         return torch._C._cuda_getCurrentRawStream(here)
     if isinstance(stream, int):
         return stream
+    if device >= 0 and getattr(stream, "device_index", device) != device:
+        raise ValueError(f"tensors on cuda:{device}, a stream of cuda:{stream.device_index}")
     return stream.cuda_stream
 
 

@@ -19,3 +19,18 @@ def test_a_workspace_is_as_long_as_it_says(ws):
     for call in calls(ws):
         with pytest.raises(ValueError, match="ws must be contiguous"):
             call()
+
+
+def test_a_stream_belongs_to_the_tensors_device(monkeypatch):
+    class Stream:
+        cuda_stream = 64
+
+        def __init__(self, device_index):
+            self.device_index = device_index
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert pb.stream_handle(Stream(1), 1) == 64 and pb.stream_handle(64, 1) == 64
+    with pytest.raises(ValueError, match="cuda:0"):
+        pb.stream_handle(Stream(0), 1)
+    with pytest.raises(ValueError):
+        pb.stream_handle(Stream(0), 0)
+    assert pb.stream_handle(Stream(0)) == 64                         # (of calls that don't know their tensors' device)
