@@ -722,7 +722,8 @@ typedef struct pi_norm {
  * strides, or a token's heads of one lie between those of the other; with other strides
  * an output that reaches into an operand's memory is refused, and so is one whose rows or
  * what lies between them reach into the weight.  The mean is summed in 64 bits.
- * An infinity or a NaN in a row reaches the row's outputs as the formula says.
+ * An infinity or a NaN in a row reaches the row's outputs as the formula says; a y past
+ * float32's largest value is infinite, in mx too.
  * tokens * heads is at most 2^23, for d > 2048 at most 2^21.
  * One kernel, no workspace.
  */

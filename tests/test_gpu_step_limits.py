@@ -97,3 +97,23 @@ def test_norm_between_the_rows_of_its_input(x_at, y_at):
     assert (np.abs(after[:, places] - want) <= 2.0 ** -10.9 * np.abs(want) + 2.0 ** -25).all()
     rest = [i for i in range(10) if i not in places]
     assert np.array_equal(after[:, rest], before[:, rest])
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_norm_past_float32(off):
+    """A y past float32's largest value is infinite in every output; its neighbours' blocks are as they are."""
+    d = 128
+    x = np.ones((3, d), np.float32)
+    w = np.ones(d, np.float32)
+    x[1, 40], w[40] = 50, 3e38
+    y, mx = torch.empty((3, d), device="cuda"), pb.empty_mx(3, d, pb.PI_MXFP8)
+    pb.pi_rms_norm(pb.make_norm(dev(w)), strided(x, 0, 0.0, off)[0], y=y, mx=mx)
+    torch.cuda.synchronize()
+    want = R.norm(x, w, 1e-5)
+    assert want[1, 40] > 3.5e38 > want[0, 40]
+    got = host(y)
+    assert np.isinf(got[1, 40]) and np.isfinite(np.delete(got.reshape(-1), d + 40)).all()
+    with np.errstate(over="ignore"):
+        seen = want.astype(np.float32).astype(np.float64)
+    assert np.array_equal(host(mx._keep[1]), R.scales(seen, "fp8"))
+    assert list(host(mx._keep[1])[1]) == [R.scales(want[1:2], "fp8")[0, 0], 255, *R.scales(want[1:2], "fp8")[0, 2:]]
